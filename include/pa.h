@@ -70,6 +70,7 @@ typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1, PA_E4M3 = 2, PA_I32 = 3, PA_I64
 #define PA_DEVERR_TIMEOUT 4u     /* a wait for an asynchronous page copy exceeded its bound                  */
 #define PA_DEVERR_CTX_RANGE 8u   /* context_lens[s] > max_context_len (or > 16 * block-table width)          */
 #define PA_DEVERR_PREFIX 16u     /* pa_decode_cascade: a block table does not share the prefix blocks        */
+#define PA_DEVERR_TREE 32u       /* pa_commit_tree: an accepted path is not one of the sequence's tree       */
 
 /* A strided view of caller-owned memory. Strides are in elements, not bytes.
  * Only the first ndim entries of shape/stride are read. The pointer is a
@@ -235,6 +236,126 @@ int pa_prefill(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache, con
                const pa_tensor* block_tables, const pa_tensor* query_start, const pa_tensor* context_lens,
                int32_t max_query_len, float scale, int32_t num_kv_heads, int32_t kernel, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Drafted tokens over the paged cache. A step that verifies drafted tokens writes their keys and
+ * values into the slots behind the context (pa_rope_and_cache), lets every drafted node attend over
+ * the context and over its own ancestors (pa_decode_tree), and, once the caller knows which path of
+ * the tree was accepted, moves that path's rows to the front of the drafted region (pa_commit_tree):
+ * the cache then holds the new context, ready for pa_decode, pa_prefill or the next tree.
+ * (The pages name speculative decoding among vLLM's features, "vLLM 前世今生" section 5.1, without an
+ * interface; these calls' interfaces are this library's.)
+ * ------------------------------------------------------------------------------------------- */
+
+/* Optional knobs of pa_rope_and_cache (NULL = these defaults; start from pa_rope_opts_init). */
+typedef struct pa_rope_opts {
+  int32_t interleaved;  /* 0: element i turns with i + R / 2; 1: 2 i with 2 i + 1 (R = rotated elements)   */
+  float magnitude;      /* multiplies every rotated element (1; some long-context scalings use more)       */
+  float k_scale;        /* dequantisation scales of an E4M3 cache, as in pa_reshape_and_cache              */
+  float v_scale;
+  int32_t* error_word;  /* device int32 that receives PA_DEVERR_* bits; NULL = the library's own word      */
+} pa_rope_opts;
+
+/* Fill opts with the defaults (half-split pairs, magnitude and scales 1). */
+void pa_rope_opts_init(pa_rope_opts* opts);
+
+/*
+ * pa_rope_and_cache -- rotate new tokens' queries and keys by their positions and write keys and
+ * values into the paged pool.
+ *   q_out, q      [T, Hq, D] device F16/BF16 (one dtype, that of key), last stride 1, 16-B aligned rows;
+ *                 q_out may be q itself (same strides), and both may be NULL (keys and values only).
+ *   key, value    [T, Hkv, D] as in pa_reshape_and_cache.
+ *   positions     [T] device I64, any values: a token's position (a drafted node's is its depth in the
+ *                 tree past the context, so siblings share one).
+ *   inv_freq      [R / 2] device F32: radians per position of each pair (pa_rope_inv_freq, or the
+ *                 model's own). The first R elements of a head turn, the others pass unchanged; R is a
+ *                 multiple of 8, 8 <= R <= D.
+ *   slot_mapping, k_cache, v_cache  as in pa_reshape_and_cache; slot -1 (or one outside the pool, which
+ *                 sets PA_DEVERR_BAD_SLOT) writes no key and value, its query row is rotated all the same.
+ * With a = positions[t] * inv_freq[i] (formed and reduced in float64), a pair (x, y) becomes
+ * magnitude * (x cos a - y sin a, y cos a + x sin a) in float32, rounded once: to nearest even for q_out
+ * and 16-bit caches; for E4M3 the unrounded value takes pa_reshape_and_cache's quantisation (no 16-bit
+ * rounding in between). Values are stored exactly as pa_reshape_and_cache stores them.
+ *   Limits: those of pa_reshape_and_cache, and D <= 512. T == 0 is a no-op.
+ */
+int pa_rope_and_cache(pa_tensor* q_out, const pa_tensor* q, const pa_tensor* key, const pa_tensor* value,
+                      const pa_tensor* positions, const pa_tensor* inv_freq, const pa_tensor* slot_mapping,
+                      pa_tensor* k_cache, pa_tensor* v_cache, const pa_rope_opts* opts, void* stream);
+
+/* How a model's frequencies are stretched for contexts longer than it was trained on. */
+typedef enum pa_rope_scaling {
+  PA_ROPE_PLAIN = 0,  /* theta_i = base^(-2 i / R)                                                        */
+  PA_ROPE_LINEAR = 1, /* theta_i / factor                                                                 */
+  PA_ROPE_BASE = 2,   /* base replaced by base * factor^(R / (R - 2)): the slowest pair slows by factor   */
+  PA_ROPE_BANDS = 3,  /* w = L theta_i / 2 pi turns over the trained length L: w >= high keeps theta_i,
+                         w <= low takes theta_i / factor, between them a blend linear in w
+                         (weight of theta_i: (w - low) / (high - low))                                    */
+  PA_ROPE_RAMP = 4    /* the same blend, linear in the pair's index between the (whole) indices where
+                         w = high (rounded down) and w = low (up), both kept within [0, R - 1]            */
+} pa_rope_scaling;
+
+/* Host helper: fills out[rot_dim / 2] with the frequencies in radians per position.
+ *   base > 1, factor >= 1, trained_len > 0 and 0 < low < high (PA_ROPE_BANDS, PA_ROPE_RAMP); arguments that
+ *   a kind does not use are ignored. rot_dim even, >= 2 (PA_ROPE_BASE: >= 4). Formed in float64, rounded once. */
+int pa_rope_inv_freq(float* out, int32_t rot_dim, double base, int32_t scaling, double factor, int64_t trained_len,
+                     double low, double high);
+
+/*
+ * pa_decode_tree -- attention of each sequence's drafted nodes over its paged context.
+ *   out, q        [T, Hq, D] device F16/BF16 (F16 with an F16 cache, BF16 with a BF16 cache, either with an
+ *                 E4M3 cache, where q must lie within the f16 range), last stride 1, 16-B aligned rows. Rows
+ *                 query_start[s] .. query_start[s + 1] - 1 are sequence s's n_s nodes, whose keys and values
+ *                 are the last n_s of its context_lens[s] cached tokens, in node order (write them first).
+ *                 Rows outside every sequence are neither read nor written.
+ *   k_cache, v_cache, block_tables  as in pa_decode (E4M3 with D = 128); query_start [B + 1] I32,
+ *                 context_lens [B] I32 as in pa_prefill.
+ *   tree_mask     [T, W] device I64, contiguous: bit j % 64 of word j / 64 of a node's row is set when
+ *                 the node sees node j of its sequence (itself included, where it does); bits at j >= n_s
+ *                 are ignored. n_s <= 64 W, W <= 4. NULL: a chain, node i sees nodes 0 .. i.
+ *   max_query_len host-known bound on n_s, <= 256 (<= 64 W with a mask).
+ *   softcap       0: none; > 0: a scaled score s becomes softcap * tanh(s / softcap).
+ *   opts          k_scale, v_scale, max_context_len, workspace (pa_decode_tree_workspace_bytes) and
+ *                 error_word as in pa_decode; partition_tokens must be 0, kernel and prefix_kernel -1.
+ * Every node sees all of the first context_lens[s] - n_s tokens, and of the drafted ones those that its
+ * mask names: out = softmax(scale * q K^T) V over what it sees, float32 accumulation, rounded to nearest
+ * even; a node that sees nothing gives zeros. Cached rows that no bit makes visible to a node may hold
+ * anything, infinities and NaN included, without reaching that node's row.
+ * A sequence that only the device can see is out of contract (n_s < 0, > max_query_len or
+ * > context_lens[s], a context longer than max_context_len or the table, rows outside q) sets
+ * PA_DEVERR_CTX_RANGE and its rows are left as they were; a bad block id sets PA_DEVERR_BAD_BLOCK and that
+ * sequence's rows are undefined.
+ */
+int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                   const pa_tensor* block_tables, const pa_tensor* query_start, const pa_tensor* context_lens,
+                   const pa_tensor* tree_mask, int32_t max_query_len, float scale, float softcap,
+                   int32_t num_kv_heads, const pa_decode_opts* opts, void* stream);
+
+/* Workspace bytes pa_decode_tree needs for these sizes (0 when no context is split). Host only. */
+size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t max_query_len, int32_t max_context_len);
+
+/*
+ * pa_commit_tree -- keep the accepted path of each sequence's drafted tree.
+ *   k_cache, v_cache  [num_blocks, Hkv, 16, D] contiguous, any one dtype of F16, BF16 and E4M3; a row
+ *                     (D elements) a multiple of 16 bytes.
+ *   block_tables, query_start, context_lens  as pa_decode_tree had them (n_s drafted nodes at the end of
+ *                     context_lens[s] tokens; query_start's differences alone matter).
+ *   accepted          [B, P] device I32, last stride 1: the accepted nodes in path order, strictly
+ *                     increasing (a parent comes before its children); entries at i >= accepted_lens[s]
+ *                     are not read.
+ *   accepted_lens     [B] device I32, 0 <= accepted_lens[s] <= min(P, n_s).
+ *   new_context_lens  [B] device I32, receives context_lens[s] - n_s + accepted_lens[s]; NULL = not wanted.
+ *                     Must not overlap the other arguments.
+ * Key and value rows of node accepted[s][i] move to the place of node i (in every KV head); rows behind
+ * the accepted ones keep what they hold. The blocks of the drafted region must belong to their sequence
+ * alone (copy shared ones first: pa_block_cow). A path that breaks the rules above sets PA_DEVERR_TREE,
+ * lengths out of range set PA_DEVERR_CTX_RANGE: nothing of that sequence moves and its new length is its
+ * old one. A bad block id sets PA_DEVERR_BAD_BLOCK and skips the row. error_word may be NULL (the
+ * library's own word).
+ */
+int pa_commit_tree(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor* block_tables,
+                   const pa_tensor* query_start, const pa_tensor* context_lens, const pa_tensor* accepted,
+                   const pa_tensor* accepted_lens, pa_tensor* new_context_lens, int32_t* error_word, void* stream);
+
 /* Partition size pa_decode uses when opts->partition_tokens == 0 and a workspace is given
  * (0 = no split: the batch's B * Hkv (sequence, KV head) units already fill the GPU, B * Hkv >= 592,
  * and every context fits one CTA, <= 2048 tokens). Otherwise the largest of 2048, 1024 and 512
@@ -291,8 +412,8 @@ int pa_read_device_error(uint32_t* bits, int clear);
 
 /* Host-side fault injection for testing a caller's error handling: the next `count` calls of
  * pa_reshape_and_cache, pa_decode, pa_decode_step, pa_decode_cascade, pa_decode_no_alloc,
- * pa_prefill and pa_copy_blocks that reach their first device call (every argument check passed
- * and there is work to enqueue) return PA_ERR_CUDA without any device work, as a call whose launch failed does (nothing is enqueued, pa_last_error says it was
+ * pa_prefill, pa_copy_blocks, pa_rope_and_cache, pa_decode_tree and pa_commit_tree that reach their
+ * first device call (every argument check passed and there is work to enqueue) return PA_ERR_CUDA without any device work, as a call whose launch failed does (nothing is enqueued, pa_last_error says it was
  * injected). count 0 disarms. Process-wide; thread-safe. Nothing reaches the GPU: no device-side
  * fault is ever made. Returns PA_OK, or PA_ERR_INVALID_ARG for count < 0. */
 int pa_debug_fail_next_launches(int32_t count);

@@ -35,6 +35,9 @@ PA_DEVERR_BAD_SLOT = 2
 PA_DEVERR_TIMEOUT = 4
 PA_DEVERR_CTX_RANGE = 8
 PA_DEVERR_PREFIX = 16
+PA_DEVERR_TREE = 32
+
+PA_ROPE_PLAIN, PA_ROPE_LINEAR, PA_ROPE_BASE, PA_ROPE_BANDS, PA_ROPE_RAMP = range(5)
 
 BLOCK_SIZE = 16
 
@@ -60,6 +63,11 @@ class PaDecodeOpts(ctypes.Structure):
                 ("error_word", ctypes.c_void_p), ("prefix_kernel", ctypes.c_int32)]
 
 
+class PaRopeOpts(ctypes.Structure):
+    _fields_ = [("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float), ("error_word", ctypes.c_void_p)]
+
+
 class PagedAttentionError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str):
         super().__init__(f"{where}: {status_string(status)} ({status}): {detail}")
@@ -82,6 +90,14 @@ def _load() -> ctypes.CDLL:
                                              ctypes.POINTER(PaDecodeOpts), VP]),
         "pa_decode_cascade_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32, I32]),
         "pa_prefill": (ctypes.c_int, [P, P, P, P, P, P, P, I32, F32, I32, I32, VP]),
+        "pa_rope_opts_init": (None, [ctypes.POINTER(PaRopeOpts)]),
+        "pa_rope_inv_freq": (ctypes.c_int, [ctypes.POINTER(F32), I32, ctypes.c_double, I32, ctypes.c_double, I64,
+                                            ctypes.c_double, ctypes.c_double]),
+        "pa_rope_and_cache": (ctypes.c_int, [P, P, P, P, P, P, P, P, P, ctypes.POINTER(PaRopeOpts), VP]),
+        "pa_decode_tree": (ctypes.c_int, [P, P, P, P, P, P, P, P, I32, F32, F32, I32, ctypes.POINTER(PaDecodeOpts),
+                                          VP]),
+        "pa_decode_tree_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32]),
+        "pa_commit_tree": (ctypes.c_int, [P, P, P, P, P, P, P, P, VP, VP]),
         "pa_decode_no_alloc": (ctypes.c_int, [P, P, P, P, P, P, F32, I32, ctypes.POINTER(PaDecodeOpts), VP]),
         "pa_decode_partition_tokens": (I32, [I32, I32, I32]),
         "pa_decode_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32]),
@@ -268,15 +284,85 @@ def pa_prefill(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cach
                            int(kernel), ctypes.c_void_p(_stream_handle(stream))), "pa_prefill")
 
 
+def _error_word_ptr(error_word: Optional[torch.Tensor]) -> Optional[int]:
+    if error_word is None:
+        return None
+    if not error_word.is_cuda or error_word.dtype != torch.int32:
+        raise ValueError("error_word must be a CUDA int32 tensor")
+    return error_word.data_ptr()
+
+
+def pa_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: int = PA_ROPE_PLAIN, factor: float = 1.0,
+                     trained_len: int = 0, low: float = 1.0, high: float = 32.0) -> torch.Tensor:
+    """Host helper: float32 [rot_dim / 2] rotary frequencies, radians per position (see include/pa.h)."""
+    out = torch.empty(max(0, int(rot_dim) // 2), dtype=torch.float32)
+    ptr = ctypes.cast(out.data_ptr(), ctypes.POINTER(ctypes.c_float)) if out.numel() else None
+    _check(_lib.pa_rope_inv_freq(ptr, int(rot_dim), float(base), int(scaling), float(factor), int(trained_len),
+                                 float(low), float(high)), "pa_rope_inv_freq")
+    return out
+
+
+def pa_rope_and_cache(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], key: torch.Tensor, value: torch.Tensor,
+                      positions: torch.Tensor, inv_freq: torch.Tensor, slot_mapping: torch.Tensor,
+                      k_cache: torch.Tensor, v_cache: torch.Tensor, interleaved: bool = False, magnitude: float = 1.0,
+                      k_scale: float = 1.0, v_scale: float = 1.0, error_word: Optional[torch.Tensor] = None,
+                      stream=None) -> None:
+    """Rotate new tokens' queries and keys and write keys and values into their slots (see include/pa.h)."""
+    o = PaRopeOpts()
+    _lib.pa_rope_opts_init(ctypes.byref(o))
+    o.interleaved, o.magnitude, o.k_scale, o.v_scale = int(bool(interleaved)), magnitude, k_scale, v_scale
+    o.error_word = _error_word_ptr(error_word)
+    qs = [None if t is None else ctypes.byref(as_pa_tensor(t, n)) for t, n in ((q_out, "q_out"), (q, "q"))]
+    args = [as_pa_tensor(key, "key"), as_pa_tensor(value, "value"), as_pa_tensor(positions, "positions"),
+            as_pa_tensor(inv_freq, "inv_freq"), as_pa_tensor(slot_mapping, "slot_mapping"),
+            as_pa_tensor(k_cache, "k_cache"), as_pa_tensor(v_cache, "v_cache")]
+    _check(_lib.pa_rope_and_cache(*qs, *[ctypes.byref(a) for a in args], ctypes.byref(o),
+                                  ctypes.c_void_p(_stream_handle(stream))), "pa_rope_and_cache")
+
+
+def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_tables: torch.Tensor, query_start: torch.Tensor, context_lens: torch.Tensor,
+                   tree_mask: Optional[torch.Tensor], max_query_len: int, scale: float, num_kv_heads: int,
+                   softcap: float = 0.0, opts: Optional[PaDecodeOpts] = None, stream=None, **kw) -> None:
+    """Attention of each sequence's drafted nodes over its paged context (see ``pa_decode_tree`` in
+    include/pa.h; ``tree_mask`` None is a chain). ``kw`` builds ``opts``."""
+    if opts is None:
+        opts = decode_opts(**kw)
+    elif kw:
+        raise TypeError("pass either opts or keyword options, not both")
+    args = [as_pa_tensor(out, "out"), as_pa_tensor(q, "q"), as_pa_tensor(k_cache, "k_cache"),
+            as_pa_tensor(v_cache, "v_cache"), as_pa_tensor(block_tables, "block_tables"),
+            as_pa_tensor(query_start, "query_start"), as_pa_tensor(context_lens, "context_lens")]
+    mask = None if tree_mask is None else ctypes.byref(as_pa_tensor(tree_mask, "tree_mask"))
+    _check(_lib.pa_decode_tree(*[ctypes.byref(a) for a in args], mask, int(max_query_len), float(scale),
+                               float(softcap), int(num_kv_heads), ctypes.byref(opts),
+                               ctypes.c_void_p(_stream_handle(stream))), "pa_decode_tree")
+
+
+def pa_decode_tree_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                   max_query_len: int, max_context_len: int) -> int:
+    return int(_lib.pa_decode_tree_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len,
+                                                   max_context_len))
+
+
+def pa_commit_tree(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                   query_start: torch.Tensor, context_lens: torch.Tensor, accepted: torch.Tensor,
+                   accepted_lens: torch.Tensor, new_context_lens: Optional[torch.Tensor] = None,
+                   error_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Move each sequence's accepted path to the front of its drafted region (see include/pa.h)."""
+    args = [as_pa_tensor(k_cache, "k_cache"), as_pa_tensor(v_cache, "v_cache"),
+            as_pa_tensor(block_tables, "block_tables"), as_pa_tensor(query_start, "query_start"),
+            as_pa_tensor(context_lens, "context_lens"), as_pa_tensor(accepted, "accepted"),
+            as_pa_tensor(accepted_lens, "accepted_lens")]
+    new = None if new_context_lens is None else ctypes.byref(as_pa_tensor(new_context_lens, "new_context_lens"))
+    _check(_lib.pa_commit_tree(*[ctypes.byref(a) for a in args], new, ctypes.c_void_p(_error_word_ptr(error_word)),
+                               ctypes.c_void_p(_stream_handle(stream))), "pa_commit_tree")
+
+
 def pa_selftest_bounded_wait(timeout_us: int, error_word: Optional[torch.Tensor] = None, stream=None) -> None:
     """Run the library's bounded barrier wait against a barrier nothing arrives on (see include/pa.h):
     it gives up after timeout_us and sets PA_DEVERR_TIMEOUT in error_word (or the library's word)."""
-    ptr = None
-    if error_word is not None:
-        if not error_word.is_cuda or error_word.dtype != torch.int32:
-            raise ValueError("error_word must be a CUDA int32 tensor")
-        ptr = error_word.data_ptr()
-    _check(_lib.pa_selftest_bounded_wait(int(timeout_us), ctypes.c_void_p(ptr), ctypes.c_void_p(_stream_handle(stream))),
+    _check(_lib.pa_selftest_bounded_wait(int(timeout_us), ctypes.c_void_p(_error_word_ptr(error_word)), ctypes.c_void_p(_stream_handle(stream))),
            "pa_selftest_bounded_wait")
 
 

@@ -1,6 +1,7 @@
 // C-ABI entry points of libpagedattn: argument validation, TMA descriptor encoding, dispatch.
 // Host code only. Every argument error is found here before the first device call; the kernels
-// live in decode.cu, decode_units.cu, multiquery.cu, prefill_tc.cu, cache.cu, no_alloc.cu and selftest.cu.
+// live in decode.cu, decode_units.cu, multiquery.cu, prefill_tc.cu, tree.cu, tree_commit.cu, rope.cu, cache.cu,
+// no_alloc.cu and selftest.cu.
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -92,6 +93,27 @@ int check_tensor(const pa_tensor* t, const char* name, int ndim) {
   for (int i = 0; i < ndim; ++i)
     if (t->shape[i] < 0) return fail(PA_ERR_INVALID_ARG, "%s: negative shape[%d]", name, i);
   return PA_OK;
+}
+
+// Whether the memory spans of two tensors (first to last element) share a byte. Host arithmetic only.
+bool overlap(const pa_tensor* a, const pa_tensor* b) {
+  uintptr_t lo[2], hi[2];
+  const pa_tensor* t[2] = {a, b};
+  for (int k = 0; k < 2; ++k) {
+    int64_t last = 0;
+    for (int i = 0; i < t[k]->ndim; ++i) {
+      int64_t d = 0;
+      if (t[k]->shape[i] == 0) return false;
+      if (__builtin_mul_overflow(t[k]->shape[i] - 1, t[k]->stride[i], &d) || d < 0 || __builtin_add_overflow(last, d, &last))
+        return true;  // not a span that can be placed: let the caller refuse it
+    }
+    int64_t bytes = 0;
+    if (__builtin_add_overflow(last, int64_t{1}, &last) || __builtin_mul_overflow(last, elem_bytes(t[k]->dtype), &bytes))
+      return true;
+    lo[k] = reinterpret_cast<uintptr_t>(t[k]->data);
+    hi[k] = lo[k] + static_cast<uintptr_t>(bytes);
+  }
+  return lo[0] < hi[1] && lo[1] < hi[0];
 }
 
 // ---- TMA descriptor encoding -----------------------------------------------------------------
@@ -810,6 +832,372 @@ int pa_decode_step(pa_tensor* out, const pa_tensor* q, const pa_tensor* key, con
   if (!key || !value || !slot_mapping) return fail(PA_ERR_INVALID_ARG, "key, value and slot_mapping are required");
   return decode_impl(out, q, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads, opts, stream, key,
                      value, slot_mapping);
+}
+
+}  // extern "C"
+
+extern "C" {
+
+void pa_rope_opts_init(pa_rope_opts* o) {
+  if (!o) return;
+  std::memset(o, 0, sizeof(*o));
+  o->magnitude = 1.0f;
+  o->k_scale = 1.0f;
+  o->v_scale = 1.0f;
+}
+
+int pa_rope_inv_freq(float* out, int32_t rot_dim, double base, int32_t scaling, double factor, int64_t trained_len,
+                     double low, double high) {
+  if (!out) return fail(PA_ERR_INVALID_ARG, "out is NULL");
+  if (rot_dim < 2 || rot_dim % 2) return fail(PA_ERR_INVALID_ARG, "rot_dim %d must be even and >= 2", rot_dim);
+  if (!(std::isfinite(base) && base > 1.0)) return fail(PA_ERR_INVALID_ARG, "base must be finite and > 1");
+  if (scaling < PA_ROPE_PLAIN || scaling > PA_ROPE_RAMP) return fail(PA_ERR_INVALID_ARG, "unknown scaling %d", scaling);
+  if (scaling != PA_ROPE_PLAIN && !(std::isfinite(factor) && factor >= 1.0))
+    return fail(PA_ERR_INVALID_ARG, "factor must be finite and >= 1");
+  const bool blend = scaling == PA_ROPE_BANDS || scaling == PA_ROPE_RAMP;
+  if (blend && !(trained_len > 0 && std::isfinite(high) && low > 0.0 && low < high))
+    return fail(PA_ERR_INVALID_ARG, "trained_len must be > 0 and 0 < low < high");
+  if (scaling == PA_ROPE_BASE) {
+    if (rot_dim < 4) return fail(PA_ERR_INVALID_ARG, "rot_dim must be >= 4 to scale the base");
+    base *= std::pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2));
+    if (!std::isfinite(base)) return fail(PA_ERR_INVALID_ARG, "the scaled base overflows");
+  }
+  const double two_pi = 6.283185307179586;
+  // The (real) pair index whose wave turns w times over the trained length.
+  auto index_of = [&](double w) { return rot_dim * std::log(trained_len / (w * two_pi)) / (2.0 * std::log(base)); };
+  double i0 = 0.0, i1 = 1.0;
+  if (scaling == PA_ROPE_RAMP) {
+    i0 = std::min(std::max(std::floor(index_of(high)), 0.0), rot_dim - 1.0);
+    i1 = std::min(std::max(std::ceil(index_of(low)), 0.0), rot_dim - 1.0);
+    if (i1 <= i0) i1 = i0 + 0.001;  // one index: a step just behind it
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double theta = std::pow(base, -2.0 * i / rot_dim);
+    double keep = 1.0;  // the weight of the unscaled frequency
+    if (scaling == PA_ROPE_LINEAR) keep = 0.0;
+    if (scaling == PA_ROPE_BANDS) keep = (trained_len * theta / two_pi - low) / (high - low);
+    if (scaling == PA_ROPE_RAMP) keep = 1.0 - (i - i0) / (i1 - i0);
+    keep = std::min(std::max(keep, 0.0), 1.0);
+    out[i] = static_cast<float>(keep == 1.0 ? theta : theta * keep + theta / factor * (1.0 - keep));
+  }
+  return ok();
+}
+
+int pa_rope_and_cache(pa_tensor* q_out, const pa_tensor* q, const pa_tensor* key, const pa_tensor* value,
+                      const pa_tensor* positions, const pa_tensor* inv_freq, const pa_tensor* slot_mapping,
+                      pa_tensor* k_cache, pa_tensor* v_cache, const pa_rope_opts* opts_in, void* stream) {
+  pa_rope_opts opts;
+  pa_rope_opts_init(&opts);
+  if (opts_in) opts = *opts_in;
+  int st;
+  if ((st = check_tensor(key, "key", 3)) || (st = check_tensor(value, "value", 3)) ||
+      (st = check_tensor(positions, "positions", 1)) || (st = check_tensor(inv_freq, "inv_freq", 1)) ||
+      (st = check_tensor(slot_mapping, "slot_mapping", 1)) || (st = check_tensor(k_cache, "k_cache", 4)) ||
+      (st = check_tensor(v_cache, "v_cache", 4)))
+    return st;
+  if ((q == nullptr) != (q_out == nullptr)) return fail(PA_ERR_INVALID_ARG, "q and q_out are given together or not at all");
+  if (q && ((st = check_tensor(q, "q", 3)) || (st = check_tensor(q_out, "q_out", 3)))) return st;
+  const int64_t T = key->shape[0], Hkv = key->shape[1], D = key->shape[2];
+  if (key->dtype != PA_F16 && key->dtype != PA_BF16)
+    return fail(PA_ERR_INVALID_ARG, "key dtype %s; expected F16 or BF16", dtype_name(key->dtype));
+  if (value->dtype != key->dtype) return fail(PA_ERR_INVALID_ARG, "value dtype differs from key dtype");
+  for (int i = 0; i < 3; ++i)
+    if (value->shape[i] != key->shape[i]) return fail(PA_ERR_INVALID_ARG, "value shape differs from key shape");
+  if (q) {
+    if (q->dtype != key->dtype || q_out->dtype != key->dtype)
+      return fail(PA_ERR_INVALID_ARG, "q and q_out must have key's dtype");
+    for (int i = 0; i < 3; ++i)
+      if (q_out->shape[i] != q->shape[i]) return fail(PA_ERR_INVALID_ARG, "q_out shape differs from q shape");
+    if (q->shape[0] != T || q->shape[2] != D) return fail(PA_ERR_INVALID_ARG, "q must be [num_tokens, num_q_heads, head_dim]");
+  }
+  if (positions->dtype != PA_I64 || positions->shape[0] != T) return fail(PA_ERR_INVALID_ARG, "positions must be I64 [num_tokens]");
+  if (slot_mapping->dtype != PA_I64 || slot_mapping->shape[0] != T)
+    return fail(PA_ERR_INVALID_ARG, "slot_mapping must be I64 [num_tokens]");
+  if (inv_freq->dtype != PA_F32) return fail(PA_ERR_INVALID_ARG, "inv_freq dtype must be F32");
+  if (T > 0x7fffffff) return fail(PA_ERR_INVALID_ARG, "too many tokens (%lld)", (long long)T);
+  if (k_cache->dtype != v_cache->dtype) return fail(PA_ERR_INVALID_ARG, "k_cache and v_cache dtypes differ");
+  const int cd = k_cache->dtype;
+  if (cd != key->dtype && cd != PA_E4M3)
+    return fail(PA_ERR_INVALID_ARG, "cache dtype %s does not match key dtype %s (or E4M3)", dtype_name(cd),
+                dtype_name(key->dtype));
+  for (int i = 0; i < 4; ++i)
+    if (v_cache->shape[i] != k_cache->shape[i]) return fail(PA_ERR_INVALID_ARG, "v_cache shape differs from k_cache");
+  if (k_cache->shape[1] != Hkv || k_cache->shape[2] != PA_BLOCK_SIZE || k_cache->shape[3] != D)
+    return fail(PA_ERR_INVALID_ARG, "cache shape must be [num_blocks, %lld, 16, %lld]", (long long)Hkv, (long long)D);
+  if (!is_contiguous(k_cache) || !is_contiguous(v_cache)) return fail(PA_ERR_INVALID_ARG, "caches must be contiguous");
+  if (D % 8 != 0 || D <= 0 || D > 512) return fail(PA_ERR_UNSUPPORTED, "head_dim %lld is not a multiple of 8 in [8, 512]", (long long)D);
+  const int64_t half = inv_freq->shape[0];
+  if (half <= 0 || half > D / 2) return fail(PA_ERR_INVALID_ARG, "inv_freq has %lld entries; head_dim is %lld", (long long)half, (long long)D);
+  if (half % 4) return fail(PA_ERR_UNSUPPORTED, "%lld rotated elements: not a multiple of 8", (long long)(2 * half));
+  if (Hkv > 65535 || (q && q->shape[1] > 65535)) return fail(PA_ERR_UNSUPPORTED, "more than 65535 heads");
+  if (checked_product({k_cache->shape[0], Hkv, PA_BLOCK_SIZE, D, 2}) < 0)
+    return fail(PA_ERR_UNSUPPORTED, "pool too large (its size does not fit in 64 bits)");
+  if (!std::isfinite(opts.magnitude)) return fail(PA_ERR_INVALID_ARG, "magnitude must be finite");
+  if (T == 0) return ok();
+  const pa_tensor* rows[4] = {key, value, q, q_out};
+  for (const pa_tensor* t : rows) {
+    if (!t || t->shape[1] == 0) continue;
+    if (t->stride[2] != 1 || !aligned(t->data, 16) || t->stride[0] % 8 || t->stride[1] % 8)
+      return fail(PA_ERR_INVALID_ARG, "q, q_out, key and value rows must be contiguous and 16-byte aligned");
+    if (!t->data) return fail(PA_ERR_INVALID_ARG, "NULL data pointer");
+  }
+  if ((positions->stride[0] != 1 || slot_mapping->stride[0] != 1) && T > 1)
+    return fail(PA_ERR_INVALID_ARG, "positions and slot_mapping must be contiguous");
+  if (inv_freq->stride[0] != 1) return fail(PA_ERR_INVALID_ARG, "inv_freq must be contiguous");
+  if (!aligned(k_cache->data, 16) || !aligned(v_cache->data, 16))
+    return fail(PA_ERR_INVALID_ARG, "caches must be 16-byte aligned");
+  if (!positions->data || !inv_freq->data || !slot_mapping->data || !k_cache->data || !v_cache->data)
+    return fail(PA_ERR_INVALID_ARG, "NULL data pointer");
+
+  pa::RopeParams p{};
+  p.key = key->data;
+  p.value = value->data;
+  p.k_stride_t = key->stride[0];
+  p.k_stride_h = key->stride[1];
+  p.v_stride_t = value->stride[0];
+  p.v_stride_h = value->stride[1];
+  if (q) {
+    p.q = q->data;
+    p.q_out = q_out->data;
+    p.q_stride_t = q->stride[0];
+    p.q_stride_h = q->stride[1];
+    p.qo_stride_t = q_out->stride[0];
+    p.qo_stride_h = q_out->stride[1];
+    p.num_q_heads = static_cast<int32_t>(q->shape[1]);
+  }
+  if (p.num_q_heads == 0 && Hkv == 0) return ok();
+  p.positions = static_cast<const int64_t*>(positions->data);
+  p.inv_freq = static_cast<const float*>(inv_freq->data);
+  p.slots = static_cast<const int64_t*>(slot_mapping->data);
+  p.k_cache = k_cache->data;
+  p.v_cache = v_cache->data;
+  p.num_tokens = T;
+  p.num_slots = k_cache->shape[0] * PA_BLOCK_SIZE;
+  p.num_kv_heads = static_cast<int32_t>(Hkv);
+  p.head_dim = static_cast<int32_t>(D);
+  p.rot = static_cast<int32_t>(2 * half);
+  p.interleaved = opts.interleaved != 0;
+  p.magnitude = opts.magnitude;
+  p.k_inv_scale = 1.0f;
+  p.v_inv_scale = 1.0f;
+  if (cd == PA_E4M3) {
+    if (!(std::isfinite(opts.k_scale) && opts.k_scale > 0.f && std::isfinite(opts.v_scale) && opts.v_scale > 0.f))
+      return fail(PA_ERR_INVALID_ARG, "E4M3 cache scales must be finite and > 0");
+    volatile float one = 1.0f;  // keep the reciprocal an IEEE float32 division
+    p.k_inv_scale = one / opts.k_scale;
+    p.v_inv_scale = one / opts.v_scale;
+  }
+  if (take_injected_failure()) return fail(PA_ERR_CUDA, "injected launch failure (pa_debug_fail_next_launches)");
+  p.err = opts.error_word ? reinterpret_cast<uint32_t*>(opts.error_word) : library_error_word();
+  if (!p.err) return fail(PA_ERR_CUDA, "no device error word (no current CUDA device?)");
+  const pa::KvType kv = cd == PA_E4M3 ? pa::KvType::E4M3 : (cd == PA_BF16 ? pa::KvType::BF16 : pa::KvType::F16);
+  cudaError_t e = pa::launch_rope_and_cache(key->dtype == PA_BF16, kv, p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, "rope_and_cache launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t max_query_len, int32_t max_context_len) {
+  if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_query_len <= 0 || max_context_len <= 0)
+    return 0;
+  return 0;
+}
+
+int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
+                   const pa_tensor* block_tables, const pa_tensor* query_start, const pa_tensor* context_lens,
+                   const pa_tensor* tree_mask, int32_t max_query_len, float scale, float softcap,
+                   int32_t num_kv_heads, const pa_decode_opts* opts_in, void* stream) {
+  pa_decode_opts opts;
+  pa_decode_opts_init(&opts);
+  if (opts_in) opts = *opts_in;
+  int st;
+  if ((st = check_tensor(out, "out", 3)) || (st = check_tensor(q, "q", 3)) || (st = check_tensor(k_cache, "k_cache", 4)) ||
+      (st = check_tensor(v_cache, "v_cache", 4)) || (st = check_tensor(block_tables, "block_tables", 2)) ||
+      (st = check_tensor(query_start, "query_start", 1)) || (st = check_tensor(context_lens, "context_lens", 1)))
+    return st;
+  if (tree_mask && (st = check_tensor(tree_mask, "tree_mask", 2))) return st;
+  const int64_t T = q->shape[0], Hq = q->shape[1], D = q->shape[2], B = block_tables->shape[0];
+  if (q->dtype != PA_F16 && q->dtype != PA_BF16) return fail(PA_ERR_INVALID_ARG, "q dtype must be F16 or BF16");
+  if (out->dtype != q->dtype) return fail(PA_ERR_INVALID_ARG, "out dtype differs from q dtype");
+  for (int i = 0; i < 3; ++i)
+    if (out->shape[i] != q->shape[i]) return fail(PA_ERR_INVALID_ARG, "out shape differs from q shape");
+  if (k_cache->dtype != v_cache->dtype) return fail(PA_ERR_INVALID_ARG, "k_cache and v_cache dtypes differ");
+  const int cd = k_cache->dtype;
+  if (cd != PA_F16 && cd != PA_BF16 && cd != PA_E4M3) return fail(PA_ERR_INVALID_ARG, "cache dtype must be F16, BF16 or E4M3");
+  if (cd != PA_E4M3 && cd != q->dtype)
+    return fail(PA_ERR_INVALID_ARG, "a %s cache needs a %s query (got %s)", dtype_name(cd), dtype_name(cd),
+                dtype_name(q->dtype));
+  for (int i = 0; i < 4; ++i)
+    if (v_cache->shape[i] != k_cache->shape[i]) return fail(PA_ERR_INVALID_ARG, "v_cache shape differs from k_cache");
+  if (num_kv_heads <= 0 || k_cache->shape[1] != num_kv_heads || Hq % num_kv_heads)
+    return fail(PA_ERR_INVALID_ARG, "num_kv_heads must equal k_cache.shape[1] and divide num_q_heads");
+  if (k_cache->shape[2] != PA_BLOCK_SIZE || k_cache->shape[3] != D)
+    return fail(PA_ERR_INVALID_ARG, "cache shape must be [num_blocks, Hkv, 16, %lld]", (long long)D);
+  if (!is_contiguous(k_cache) || !is_contiguous(v_cache)) return fail(PA_ERR_INVALID_ARG, "caches must be contiguous");
+  if (block_tables->dtype != PA_I32 || (block_tables->stride[1] != 1 && block_tables->shape[1] > 1))
+    return fail(PA_ERR_INVALID_ARG, "block_tables must be I32 [num_seqs, max_blocks], last stride 1");
+  if (query_start->dtype != PA_I32 || query_start->shape[0] != B + 1 || (query_start->stride[0] != 1 && B > 0))
+    return fail(PA_ERR_INVALID_ARG, "query_start must be contiguous I32 [num_seqs + 1]");
+  if (context_lens->dtype != PA_I32 || context_lens->shape[0] != B || (context_lens->stride[0] != 1 && B > 1))
+    return fail(PA_ERR_INVALID_ARG, "context_lens must be contiguous I32 [num_seqs]");
+  if (tree_mask) {
+    if (tree_mask->dtype != PA_I64 || tree_mask->shape[0] != T || !is_contiguous(tree_mask))
+      return fail(PA_ERR_INVALID_ARG, "tree_mask must be contiguous I64 [num_tokens, words]");
+    if (tree_mask->shape[1] < 1 || tree_mask->shape[1] > pa::kTreeMaskWords)
+      return fail(PA_ERR_UNSUPPORTED, "tree_mask has %lld words; 1 to %d are supported", (long long)tree_mask->shape[1],
+                  pa::kTreeMaskWords);
+  }
+  if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale must be finite");
+  if (!(std::isfinite(softcap) && softcap >= 0.f)) return fail(PA_ERR_INVALID_ARG, "softcap must be finite and >= 0");
+  if (T == 0 || B == 0 || Hq == 0) return ok();
+  if (max_query_len <= 0) return fail(PA_ERR_INVALID_ARG, "max_query_len must be > 0");
+  if (max_query_len > pa::kTreeMaxNodes || (tree_mask && max_query_len > 64 * tree_mask->shape[1]))
+    return fail(PA_ERR_UNSUPPORTED, "max_query_len %d exceeds %d nodes, or 64 per word of tree_mask", max_query_len,
+                pa::kTreeMaxNodes);
+  if (T > 0x7fffffff) return fail(PA_ERR_INVALID_ARG, "too many rows (%lld)", (long long)T);
+  const int64_t NB = k_cache->shape[0], G = Hq / num_kv_heads;
+  if (NB <= 0) return fail(PA_ERR_INVALID_ARG, "empty pool");
+  if (NB > 0x7fffffffLL / 16 / num_kv_heads) return fail(PA_ERR_UNSUPPORTED, "pool too large (rows exceed 2^31)");
+  if (B > 65535 || num_kv_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "num_seqs and num_kv_heads must be <= 65535");
+  const pa::KvType kv = cd == PA_E4M3 ? pa::KvType::E4M3 : (cd == PA_BF16 ? pa::KvType::BF16 : pa::KvType::F16);
+  const pa::QType qt = q->dtype == PA_BF16 ? pa::QType::BF16 : pa::QType::F16;
+  if (G > 16 || !pa::tree_supported(kv, static_cast<int>(std::min<int64_t>(D, 0x7fffffff)), static_cast<int>(G)))
+    return fail(PA_ERR_UNSUPPORTED, "no kernel for head_dim %lld, cache %s, group %lld", (long long)D, dtype_name(cd), (long long)G);
+  if (q->stride[2] != 1 || out->stride[2] != 1 || !aligned(q->data, 16) || !aligned(out->data, 16) ||
+      q->stride[0] % 8 || q->stride[1] % 8 || out->stride[0] % 8 || out->stride[1] % 8)
+    return fail(PA_ERR_INVALID_ARG, "q/out rows must be contiguous and 16-byte aligned");
+  if (!aligned(k_cache->data, 128) || !aligned(v_cache->data, 128))
+    return fail(PA_ERR_INVALID_ARG, "caches must be 128-byte aligned");
+  if (block_tables->shape[1] <= 0) return fail(PA_ERR_INVALID_ARG, "block_tables has no columns");
+  if (!out->data || !q->data || !k_cache->data || !v_cache->data || !block_tables->data || !query_start->data ||
+      !context_lens->data || (tree_mask && !tree_mask->data))
+    return fail(PA_ERR_INVALID_ARG, "NULL data pointer");
+  if (tree_mask && !aligned(tree_mask->data, 8)) return fail(PA_ERR_INVALID_ARG, "tree_mask must be 8-byte aligned");
+  float k_scale = 1.f, v_scale = 1.f;
+  if (cd == PA_E4M3) {
+    k_scale = opts.k_scale;
+    v_scale = opts.v_scale;
+    if (!(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
+      return fail(PA_ERR_INVALID_ARG, "E4M3 cache scales must be finite and > 0");
+  }
+  if (opts.max_context_len < 0) return fail(PA_ERR_INVALID_ARG, "max_context_len < 0");
+  if (opts.partition_tokens != 0 || opts.kernel != -1 || opts.prefix_kernel != -1)
+    return fail(PA_ERR_INVALID_ARG, "pa_decode_tree splits contexts and picks its kernel itself: partition_tokens must be "
+                                    "0, kernel and prefix_kernel -1");
+  const int64_t max_blocks = std::min<int64_t>(block_tables->shape[1], 0x7fffffff / 16);
+  const int64_t max_ctx = opts.max_context_len > 0 ? std::min<int64_t>(opts.max_context_len, max_blocks * 16) : max_blocks * 16;
+
+  pa::TreeParams p{};
+  p.out = out->data;
+  p.q = q->data;
+  p.q_stride_t = q->stride[0];
+  p.q_stride_h = q->stride[1];
+  p.o_stride_t = out->stride[0];
+  p.o_stride_h = out->stride[1];
+  p.k_cache = k_cache->data;
+  p.v_cache = v_cache->data;
+  p.block_tables = static_cast<const int32_t*>(block_tables->data);
+  p.bt_stride = block_tables->stride[0];
+  p.query_start = static_cast<const int32_t*>(query_start->data);
+  p.context_lens = static_cast<const int32_t*>(context_lens->data);
+  if (tree_mask) {
+    p.mask = static_cast<const uint64_t*>(tree_mask->data);
+    p.mask_words = static_cast<int32_t>(tree_mask->shape[1]);
+  }
+  p.num_tokens = static_cast<int32_t>(T);
+  p.num_seqs = static_cast<int32_t>(B);
+  p.num_blocks = static_cast<int32_t>(NB);
+  p.num_kv_heads = num_kv_heads;
+  p.group = static_cast<int32_t>(G);
+  p.max_blocks = static_cast<int32_t>(max_blocks);
+  p.max_query_len = max_query_len;
+  p.max_context_len = static_cast<int32_t>(max_ctx);
+  p.score_scale = scale * k_scale;
+  p.softcap = softcap;
+  p.v_scale = v_scale;
+  if (take_injected_failure()) return fail(PA_ERR_CUDA, "injected launch failure (pa_debug_fail_next_launches)");
+  p.err = opts.error_word ? reinterpret_cast<uint32_t*>(opts.error_word) : library_error_word();
+  if (!p.err) return fail(PA_ERR_CUDA, "no device error word (no current CUDA device?)");
+  cudaError_t e = pa::launch_decode_tree(kv, qt, static_cast<int>(D), p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, "decode_tree launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+int pa_commit_tree(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor* block_tables,
+                   const pa_tensor* query_start, const pa_tensor* context_lens, const pa_tensor* accepted,
+                   const pa_tensor* accepted_lens, pa_tensor* new_context_lens, int32_t* error_word, void* stream) {
+  int st;
+  if ((st = check_tensor(k_cache, "k_cache", 4)) || (st = check_tensor(v_cache, "v_cache", 4)) ||
+      (st = check_tensor(block_tables, "block_tables", 2)) || (st = check_tensor(query_start, "query_start", 1)) ||
+      (st = check_tensor(context_lens, "context_lens", 1)) || (st = check_tensor(accepted, "accepted", 2)) ||
+      (st = check_tensor(accepted_lens, "accepted_lens", 1)))
+    return st;
+  if (new_context_lens && (st = check_tensor(new_context_lens, "new_context_lens", 1))) return st;
+  const int64_t B = block_tables->shape[0], Hkv = k_cache->shape[1], D = k_cache->shape[3], NB = k_cache->shape[0];
+  if (k_cache->dtype != PA_F16 && k_cache->dtype != PA_BF16 && k_cache->dtype != PA_E4M3)
+    return fail(PA_ERR_INVALID_ARG, "cache dtype must be F16, BF16 or E4M3");
+  if (k_cache->dtype != v_cache->dtype) return fail(PA_ERR_INVALID_ARG, "k_cache and v_cache dtypes differ");
+  for (int i = 0; i < 4; ++i)
+    if (v_cache->shape[i] != k_cache->shape[i]) return fail(PA_ERR_INVALID_ARG, "v_cache shape differs from k_cache");
+  if (k_cache->shape[2] != PA_BLOCK_SIZE) return fail(PA_ERR_INVALID_ARG, "cache shape must be [num_blocks, Hkv, 16, D]");
+  if (!is_contiguous(k_cache) || !is_contiguous(v_cache)) return fail(PA_ERR_INVALID_ARG, "caches must be contiguous");
+  if (block_tables->dtype != PA_I32 || (block_tables->stride[1] != 1 && block_tables->shape[1] > 1))
+    return fail(PA_ERR_INVALID_ARG, "block_tables must be I32 [num_seqs, max_blocks], last stride 1");
+  if (query_start->dtype != PA_I32 || query_start->shape[0] != B + 1 || (query_start->stride[0] != 1 && B > 0))
+    return fail(PA_ERR_INVALID_ARG, "query_start must be contiguous I32 [num_seqs + 1]");
+  if (context_lens->dtype != PA_I32 || context_lens->shape[0] != B || (context_lens->stride[0] != 1 && B > 1))
+    return fail(PA_ERR_INVALID_ARG, "context_lens must be contiguous I32 [num_seqs]");
+  if (accepted->dtype != PA_I32 || accepted->shape[0] != B || (accepted->stride[1] != 1 && accepted->shape[1] > 1))
+    return fail(PA_ERR_INVALID_ARG, "accepted must be I32 [num_seqs, path], last stride 1");
+  if (accepted_lens->dtype != PA_I32 || accepted_lens->shape[0] != B || (accepted_lens->stride[0] != 1 && B > 1))
+    return fail(PA_ERR_INVALID_ARG, "accepted_lens must be contiguous I32 [num_seqs]");
+  if (new_context_lens) {
+    if (new_context_lens->dtype != PA_I32 || new_context_lens->shape[0] != B || (new_context_lens->stride[0] != 1 && B > 1))
+      return fail(PA_ERR_INVALID_ARG, "new_context_lens must be contiguous I32 [num_seqs]");
+  }
+  if (B == 0 || Hkv == 0) return ok();
+  const int64_t row_bytes = checked_product({D, elem_bytes(k_cache->dtype)});
+  if (row_bytes <= 0 || row_bytes % 16 || row_bytes > (1 << 20))
+    return fail(PA_ERR_UNSUPPORTED, "rows of %lld bytes: a multiple of 16 is needed", (long long)row_bytes);
+  if (checked_product({NB, Hkv, PA_BLOCK_SIZE, row_bytes}) < 0)
+    return fail(PA_ERR_UNSUPPORTED, "pool too large (its size does not fit in 64 bits)");
+  if (NB <= 0) return fail(PA_ERR_INVALID_ARG, "empty pool");
+  if (NB > 0x7fffffff) return fail(PA_ERR_UNSUPPORTED, "pool too large (block ids exceed 2^31)");
+  if (B > 0x7fffffff || Hkv > 32767) return fail(PA_ERR_UNSUPPORTED, "too many sequences or KV heads");
+  if (accepted->shape[1] > 0x7fffffff) return fail(PA_ERR_UNSUPPORTED, "accepted paths too long");
+  if (!aligned(k_cache->data, 16) || !aligned(v_cache->data, 16)) return fail(PA_ERR_INVALID_ARG, "caches must be 16-byte aligned");
+  if (block_tables->shape[1] <= 0) return fail(PA_ERR_INVALID_ARG, "block_tables has no columns");
+  if (!k_cache->data || !v_cache->data || !block_tables->data || !query_start->data || !context_lens->data ||
+      !accepted_lens->data || (accepted->shape[1] > 0 && !accepted->data) || (new_context_lens && !new_context_lens->data))
+    return fail(PA_ERR_INVALID_ARG, "NULL data pointer");
+  if (new_context_lens) {
+    const pa_tensor* ins[5] = {block_tables, query_start, context_lens, accepted, accepted_lens};
+    for (const pa_tensor* t : ins)
+      if (overlap(new_context_lens, t)) return fail(PA_ERR_INVALID_ARG, "new_context_lens overlaps another argument");
+  }
+  pa::CommitParams p{};
+  p.k_cache = k_cache->data;
+  p.v_cache = v_cache->data;
+  p.block_tables = static_cast<const int32_t*>(block_tables->data);
+  p.bt_stride = block_tables->stride[0];
+  p.query_start = static_cast<const int32_t*>(query_start->data);
+  p.context_lens = static_cast<const int32_t*>(context_lens->data);
+  p.accepted = static_cast<const int32_t*>(accepted->data);
+  p.accepted_stride = accepted->stride[0];
+  p.accepted_lens = static_cast<const int32_t*>(accepted_lens->data);
+  p.new_context_lens = new_context_lens ? static_cast<int32_t*>(new_context_lens->data) : nullptr;
+  p.num_seqs = static_cast<int32_t>(B);
+  p.num_blocks = static_cast<int32_t>(NB);
+  p.num_kv_heads = static_cast<int32_t>(Hkv);
+  p.max_blocks = static_cast<int32_t>(std::min<int64_t>(block_tables->shape[1], 0x7fffffff / 16));
+  p.path_len = static_cast<int32_t>(accepted->shape[1]);
+  p.row_bytes = static_cast<int32_t>(row_bytes);
+  if (take_injected_failure()) return fail(PA_ERR_CUDA, "injected launch failure (pa_debug_fail_next_launches)");
+  p.err = error_word ? reinterpret_cast<uint32_t*>(error_word) : library_error_word();
+  if (!p.err) return fail(PA_ERR_CUDA, "no device error word (no current CUDA device?)");
+  cudaError_t e = pa::launch_commit_tree(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(PA_ERR_CUDA, "commit_tree launch: %s", cudaGetErrorString(e));
+  return ok();
 }
 
 }  // extern "C"

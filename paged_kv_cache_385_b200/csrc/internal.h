@@ -152,6 +152,78 @@ struct CopyParams {
 };
 cudaError_t launch_copy_blocks(const CopyParams& p, cudaStream_t stream);
 
+// Rotary positions and the cache write (rope.cu). Strides are in elements.
+struct RopeParams {
+  void* q_out;    // [T, Hq, D], or null
+  const void* q;
+  const void* key;
+  const void* value;
+  int64_t qo_stride_t, qo_stride_h, q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h;
+  const int64_t* positions;
+  const float* inv_freq;  // [rot / 2]
+  const int64_t* slots;
+  void* k_cache;
+  void* v_cache;
+  int64_t num_tokens;
+  int64_t num_slots;
+  int32_t num_q_heads;  // 0 when q is null
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t rot;  // rotated elements of a head, a multiple of 8
+  int32_t interleaved;
+  float magnitude;
+  float k_inv_scale, v_inv_scale;
+  uint32_t* err;
+};
+cudaError_t launch_rope_and_cache(int src_bf16, KvType cache, const RopeParams& p, cudaStream_t stream);
+
+// Attention of drafted nodes over the paged context (tree.cu).
+struct TreeParams {
+  void* out;  // [T, Hq, D]
+  const void* q;
+  int64_t q_stride_t, q_stride_h, o_stride_t, o_stride_h;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  int64_t bt_stride;
+  const int32_t* query_start;   // [B + 1]
+  const int32_t* context_lens;  // [B]
+  const uint64_t* mask;         // [T, mask_words], or null: a chain
+  int32_t mask_words;
+  int32_t num_tokens;  // T
+  int32_t num_seqs, num_blocks, num_kv_heads, group;
+  int32_t max_blocks;
+  int32_t max_query_len;
+  int32_t max_context_len;
+  float score_scale;  // scale * k_scale
+  float softcap;      // 0 = none
+  float v_scale;
+  uint32_t* err;
+};
+constexpr int kTreeMaxNodes = 256;
+constexpr int kTreeMaskWords = kTreeMaxNodes / 64;
+bool tree_supported(KvType kv, int head_dim, int group);
+cudaError_t launch_decode_tree(KvType kv, QType q, int head_dim, const TreeParams& p, cudaStream_t stream);
+
+// Accepted path of each sequence's tree moved to the front of its drafted region (tree_commit.cu).
+struct CommitParams {
+  void* k_cache;
+  void* v_cache;
+  const int32_t* block_tables;
+  int64_t bt_stride;
+  const int32_t* query_start;
+  const int32_t* context_lens;
+  const int32_t* accepted;  // [B, P]
+  int64_t accepted_stride;
+  const int32_t* accepted_lens;
+  int32_t* new_context_lens;  // null = not wanted
+  int32_t num_seqs, num_blocks, num_kv_heads, max_blocks;
+  int32_t path_len;   // P
+  int32_t row_bytes;  // D elements, a multiple of 16
+  uint32_t* err;
+};
+cudaError_t launch_commit_tree(const CommitParams& p, cudaStream_t stream);
+
 uint32_t* decode_error_word();  // device address of the library's own error word
 
 // Record the reason pa_last_error() reports for this thread; returns status.

@@ -1,0 +1,240 @@
+"""pa_decode_tree on the GPU against the float64 definition (oracle/tree.py)."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_385_b200 as pa
+from tests.tree_case import TreeCase
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    pa.pa_read_device_error(clear=True)
+    yield
+    assert pa.pa_read_device_error(clear=True) == 0
+
+
+def check(c: TreeCase, got: torch.Tensor):
+    want, weight = c.oracle()
+    n = c.start_host[-1]
+    err = np.abs(got.double().cpu().numpy()[:n] - want[:n])
+    over = err > c.bound(want, weight)[:n]
+    assert not over.any(), (f"{int(over.sum())} of {over.size} values off, worst {np.nanmax(err):.3g} at "
+                            f"{np.argwhere(over)[0].tolist()}")
+    assert torch.all(got[n:] == 77.0)  # rows behind the last sequence
+
+
+CASES = {
+    # name: (kv, d, hkv, group, nodes per sequence, context per sequence, options)
+    "one_token": ("f16", 64, 1, 1, [1], [1], {}),
+    "one_token_128": ("bf16", 128, 2, 4, [1, 1], [1, 300], {}),
+    "small": ("bf16", 128, 2, 4, [8], [100], {}),
+    "whole_context_drafted": ("f16", 128, 1, 2, [16, 3, 64, 65], [16, 3, 64, 65], {}),
+    "ragged": ("bf16", 128, 2, 4, [5, 0, 33, 1, 64], [5, 17, 1000, 63, 321], {}),
+    "chain": ("f16", 128, 2, 4, [7, 64, 1], [500, 70, 65], {"masks": None}),
+    "mha": ("f16", 128, 3, 1, [6, 17], [290, 48], {}),
+    "group3": ("bf16", 128, 2, 3, [43, 9], [333, 31], {}),
+    "group7_d64": ("f16", 64, 2, 7, [19, 37], [129, 400], {}),
+    "group16": ("f16", 128, 1, 16, [8, 9], [256, 77], {}),
+    "two_words": ("bf16", 128, 1, 2, [128, 100, 65], [200, 1100, 66], {}),
+    "four_words": ("f16", 128, 1, 1, [256, 193], [1030, 193], {}),
+    "four_words_chain": ("bf16", 64, 1, 5, [256], [300], {"masks": None}),
+    "d64": ("bf16", 64, 4, 2, [13, 1, 50], [250, 16, 52], {}),
+    "e4m3": ("e4m3", 128, 2, 8, [32, 7], [700, 65], {}),
+    "e4m3_f16_query": ("e4m3", 128, 1, 4, [64, 5], [64, 2000], {"q": "f16"}),
+    "e4m3_chain": ("e4m3", 128, 2, 3, [9, 1, 130], [1000, 1, 131], {"masks": None, "q": "f16"}),
+    "capped": ("f16", 128, 2, 4, [12, 3], [400, 90], {"softcap": 2.0}),
+    "capped_d64": ("bf16", 64, 2, 2, [12, 65], [400, 90], {"softcap": 30.0}),
+    "capped_e4m3": ("e4m3", 128, 1, 8, [20], [300], {"softcap": 5.0}),
+    "negative_scale": ("f16", 128, 1, 4, [9, 2], [150, 40], {"scale": -0.08}),
+    "zero_scale": ("bf16", 128, 1, 4, [9], [150], {"scale": 0.0}),
+    "long_split": ("bf16", 128, 1, 4, [10], [9001], {}),
+    "long_split_e4m3": ("e4m3", 128, 1, 8, [3], [8000], {}),
+    "long_split_d64": ("f16", 64, 2, 1, [5, 2], [7000, 33], {}),
+    "many_short": ("f16", 64, 2, 2, [3, 1, 2, 5] * 40, [4, 1, 70, 33] * 40, {}),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_against_the_definition(name):
+    kv, d, hkv, group, counts, lens, opts = CASES[name]
+    c = TreeCase(kv, d, hkv, group, counts, lens, seed=len(name), extra_rows=3, **opts).to_device()
+    check(c, c.run())
+
+
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 63, 64, 65, 127, 128, 129])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_tree_at_every_offset_of_a_tile(kv, n):
+    """Contexts that end at, before and behind page and key-block borders, the tree straddling them."""
+    lens = [n, n + 1, n + 15, n + 31, n + 48, n + 63, n + 64]
+    c = TreeCase(kv, 128, 1, 2, [n] * len(lens), lens, seed=n).to_device()
+    check(c, c.run())
+
+
+def test_rows_that_see_nothing_are_zero():
+    masks = [0, 0b10, 0, 0b1111]
+    c = TreeCase("f16", 128, 1, 4, [4], [4], masks=masks, seed=3).to_device()
+    got = c.run()
+    check(c, got)
+    assert torch.all(got[0] == 0) and torch.all(got[2] == 0)
+
+
+def test_bits_behind_the_last_node_are_ignored():
+    c = TreeCase("bf16", 128, 2, 2, [5, 70], [40, 170], seed=4).to_device()
+    got = c.run().clone()
+    full = torch.tensor(-1, dtype=torch.int64, device="cuda")
+    for s, n in enumerate(c.counts):
+        rows = c.mask[c.start_host[s]:c.start_host[s + 1]]
+        for w in range(c.words):
+            keep = max(0, min(64, n - 64 * w))
+            if keep < 64:
+                rows[:, w] |= full << keep
+    assert torch.equal(c.run(out=torch.full_like(c.out, 77.0)), got)
+    check(c, got)
+
+
+@pytest.mark.parametrize("kv", ["f16", "bf16", "e4m3"])
+@pytest.mark.parametrize("ctx", [12, 60, 1500])
+def test_masked_rows_may_hold_anything(kv, ctx):
+    """Keys and values of nodes that a node does not see are infinite or NaN: its row does not change."""
+    c = TreeCase(kv, 128, 2, 4, [12], [ctx], seed=5)
+    before = c.to_device().run().clone()
+    bad = 7  # the node that holds them: whoever sees it gives NaN, the others what they gave
+    at = ctx - 12 + bad
+    for pool, values in ((c.k_cache, (float("nan"), float("inf"))), (c.v_cache, (float("inf"), float("nan")))):
+        row = pool[int(c.bt_host[0, at // 16]), :, at % 16]
+        for h, v in enumerate(values):
+            row[h] = torch.full((128,), v).to(pool.dtype).cuda()
+    got = c.run(out=torch.full_like(c.out, 77.0))
+    sees = torch.tensor([bool(m >> bad & 1) for m in c.masks])
+    assert sees.any() and not sees.all()
+    assert torch.equal(got[:12][~sees.cuda()], before[:12][~sees.cuda()])
+    assert torch.isnan(got[:12][sees.cuda()]).all()
+
+
+def test_infinite_values_reach_the_nodes_that_see_them():
+    c = TreeCase("f16", 128, 1, 4, [6], [300], seed=6).to_device()
+    before = c.run().clone()
+    at = 300 - 6 + 3
+    c.v_cache[int(c.bt_host[0, at // 16]), 0, at % 16, 5] = float("inf")
+    c.v_cache[int(c.bt_host[0, at // 16]), 0, at % 16, 6] = float("-inf")
+    got = c.run()
+    sees = torch.tensor([bool(m >> 3 & 1) for m in c.masks]).cuda()
+    assert torch.all(got[:6][sees][..., 5] == float("inf")) and torch.all(got[:6][sees][..., 6] == float("-inf"))
+    got[:6][..., 5:7] = before[:6][..., 5:7]
+    assert torch.equal(got[:6][~sees], before[:6][~sees])
+    rest = torch.ones(128, dtype=torch.bool)
+    rest[5:7] = False
+    assert torch.equal(got[:6][..., rest.cuda()], before[:6][..., rest.cuda()])
+
+
+def test_single_nodes_agree_with_decode():
+    """One drafted node per sequence is a decode step: both within their roundings of one exact row."""
+    c = TreeCase("bf16", 128, 2, 4, [1] * 4, [1, 40, 700, 3000], seed=7).to_device()
+    got = c.run()
+    check(c, got)
+    out = torch.empty_like(c.q)
+    pa.pa_decode(out, c.q, c.k_cache, c.v_cache, c.bt, c.lens, c.scale, c.hkv, max_context_len=3000,
+                 workspace=pa.decode_workspace(4, c.hq, c.hkv, 128, 3000))
+    check(c, out)
+
+
+def test_chain_agrees_with_prefill():
+    c = TreeCase("f16", 128, 2, 4, [40, 7], [700, 90], masks=None, seed=8).to_device()
+    check(c, c.run())
+    out = torch.empty_like(c.q)
+    pa.pa_prefill(out, c.q, c.k_cache, c.v_cache, c.bt, c.start, c.lens, 40, c.scale, c.hkv)
+    check(c, out)
+
+
+def test_strided_rows():
+    c = TreeCase("bf16", 128, 2, 4, [9, 20], [100, 222], seed=9).to_device()
+    T = c.q.shape[0]
+    wide = torch.randn(T, c.hq + 4, 136, device="cuda").to(torch.bfloat16)
+    q = wide[:, 2:2 + c.hq, 8:]
+    q.copy_(c.q)
+    out = torch.full((c.hq, T, 256), 77.0, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    c.run(out=out[..., :128], q=q)
+    check(c, out[..., :128].contiguous())
+    assert torch.all(out[..., 128:] == 77.0)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_placement_and_repetition_change_nothing(kv):
+    args = (kv, 128, 2, 4, [9, 33, 1], [100, 2222, 640])
+    a = TreeCase(*args, seed=10).to_device()
+    first = a.run().clone()
+    for fill in (0, 0x7f):
+        a.out.fill_(77.0)
+        assert torch.equal(a.run(workspace=a.workspace(fill)), first)
+    b = TreeCase(*args, seed=10, order=99).to_device()
+    assert torch.equal(b.run(), first)
+
+
+def test_default_context_bound_is_the_table():
+    c = TreeCase("bf16", 128, 1, 4, [9], [100], seed=11).to_device()
+    n = pa.pa_decode_tree_workspace_bytes(1, 4, 1, 128, 9, 16 * c.bt.shape[1])
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda") if n else None
+    check(c, c.run(max_context_len=0, workspace=ws))
+
+
+def test_other_stream_and_graph():
+    c = TreeCase("bf16", 128, 2, 4, [16, 5], [900, 4000], seed=12).to_device()
+    want = c.run().clone()
+    ws = c.workspace()
+    side = torch.cuda.Stream()
+    c.out.fill_(77.0)
+    side.wait_stream(torch.cuda.current_stream())
+    c.run(workspace=ws, stream=side)
+    side.synchronize()
+    assert torch.equal(c.out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        c.run(workspace=ws)
+    # Lengths and values of a later step: the graph reads what the buffers hold then.
+    d = TreeCase("bf16", 128, 2, 4, [5, 16], [77, 3000], seed=13).to_device()
+    c.k_cache[:d.num_blocks].copy_(d.k_cache)
+    c.v_cache[:d.num_blocks].copy_(d.v_cache)
+    c.bt.fill_(-1)
+    c.bt[:, :d.bt.shape[1]].copy_(d.bt)
+    c.start.copy_(d.start), c.lens.copy_(d.lens), c.q.copy_(d.q), c.mask.copy_(d.mask)
+    for _ in range(2):
+        c.out.fill_(77.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(d, c.out)
+
+
+@pytest.mark.parametrize("kv", ["f16", "e4m3"])
+def test_out_of_contract_sequences_are_left_alone(kv):
+    """A sequence the device finds out of contract sets its bit; the others are computed."""
+    c = TreeCase(kv, 128, 2, 4, [5, 9, 6], [60, 90, 200], seed=14).to_device()
+    good = c.run().clone()
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def rerun(**kw):
+        word.zero_()
+        return c.run(out=torch.full_like(c.out, 77.0), error_word=word, **kw)
+
+    lens = c.lens.clone()
+    for bad in (4, 0, -3, 16 * c.bt.shape[1] + 1, 2 ** 31 - 1):  # shorter than its nodes, or past the table
+        c.lens[0] = bad
+        got = rerun()
+        assert int(word) == pa.PA_DEVERR_CTX_RANGE, bad
+        assert torch.all(got[:5] == 77.0) and torch.equal(got[5:20], good[5:20])
+        c.lens.copy_(lens)
+    got = rerun(max_context_len=150)
+    assert int(word) == pa.PA_DEVERR_CTX_RANGE and torch.all(got[14:20] == 77.0) and torch.equal(got[:14], good[:14])
+    start = c.start.clone()
+    for at, value in ((3, 10 ** 6), (0, -1), (3, 13)):  # rows outside q; a negative count
+        c.start[at] = value
+        rerun()
+        assert int(word) == pa.PA_DEVERR_CTX_RANGE, (at, value)
+        c.start.copy_(start)
+    c.bt[1, 2] = c.num_blocks
+    got = rerun()
+    assert int(word) == pa.PA_DEVERR_BAD_BLOCK
+    assert torch.equal(got[:5], good[:5]) and torch.equal(got[14:20], good[14:20])
+    assert pa.pa_read_device_error(clear=True) == 0
