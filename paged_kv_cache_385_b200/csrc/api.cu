@@ -243,6 +243,17 @@ size_t workspace_layout(int64_t B, int64_t Hq, int64_t D, int64_t P, size_t* ml_
   return acc + ml;
 }
 
+// Layout of the tree workspace: partial rows, then their (m, l), then a descriptor per span. 0 bytes when
+// no context can be cut.
+size_t tree_workspace(int64_t head_dim, int64_t max_ctx, int spans, size_t* ml_offset, size_t* desc_offset) {
+  if (!pa::tree_splits(max_ctx)) return 0;
+  const size_t acc = round_up(static_cast<size_t>(2 * spans) * pa::kTreeRows * static_cast<size_t>(head_dim) * sizeof(float), 256);
+  const size_t ml = round_up(static_cast<size_t>(2 * spans) * pa::kTreeRows * 2 * sizeof(float), 256);
+  if (ml_offset) *ml_offset = acc;
+  if (desc_offset) *desc_offset = acc + ml;
+  return acc + ml + round_up(static_cast<size_t>(spans) * pa::kTreeDescInts * sizeof(int32_t), 256);
+}
+
 }  // namespace
 
 namespace pa {
@@ -998,9 +1009,12 @@ int pa_rope_and_cache(pa_tensor* q_out, const pa_tensor* q, const pa_tensor* key
 
 size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                       int32_t max_query_len, int32_t max_context_len) {
-  if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_query_len <= 0 || max_context_len <= 0)
+  if (num_seqs <= 0 || num_kv_heads <= 0 || num_q_heads < num_kv_heads || head_dim <= 0 || max_query_len <= 0 ||
+      max_context_len <= 0)
     return 0;
-  return 0;
+  return tree_workspace(head_dim, max_context_len,
+                        pa::tree_spans(num_seqs, num_kv_heads, num_q_heads / num_kv_heads, max_query_len, max_context_len),
+                        nullptr, nullptr);
 }
 
 int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
@@ -1115,10 +1129,30 @@ int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache,
   p.score_scale = scale * k_scale;
   p.softcap = softcap;
   p.v_scale = v_scale;
+  p.spans = pa::tree_spans(B, num_kv_heads, p.group, max_query_len, max_ctx);
+  size_t ml_off = 0, desc_off = 0;
+  if (const size_t need = tree_workspace(D, max_ctx, p.spans, &ml_off, &desc_off)) {
+    const size_t have = opts.workspace ? opts.workspace_bytes : 0;
+    if (have < need)
+      return fail(PA_ERR_WORKSPACE, "contexts of up to %lld tokens need a workspace of %zu bytes (got %zu)", (long long)max_ctx,
+                  need, have);
+    if (!aligned(opts.workspace, 256)) return fail(PA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    char* ws = static_cast<char*>(opts.workspace);
+    p.ws_acc = reinterpret_cast<float*>(ws);
+    p.ws_ml = reinterpret_cast<float2*>(ws + ml_off);
+    p.ws_desc = reinterpret_cast<int32_t*>(ws + desc_off);
+  }
   if (take_injected_failure()) return fail(PA_ERR_CUDA, "injected launch failure (pa_debug_fail_next_launches)");
   p.err = opts.error_word ? reinterpret_cast<uint32_t*>(opts.error_word) : library_error_word();
   if (!p.err) return fail(PA_ERR_CUDA, "no device error word (no current CUDA device?)");
-  cudaError_t e = pa::launch_decode_tree(kv, qt, static_cast<int>(D), p, static_cast<cudaStream_t>(stream));
+  cudaError_t e;
+  if (kv == pa::KvType::E4M3) {
+    e = pa::launch_decode_tree(kv, qt, static_cast<int>(D), p, static_cast<cudaStream_t>(stream));
+  } else {
+    CUtensorMap km, vm;
+    if ((st = encode_pool_map(&km, k_cache, elem_bytes(cd))) || (st = encode_pool_map(&vm, v_cache, elem_bytes(cd)))) return st;
+    e = pa::launch_decode_tree_tc(kv, static_cast<int>(D), km, vm, p, static_cast<cudaStream_t>(stream));
+  }
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "decode_tree launch: %s", cudaGetErrorString(e));
   return ok();
 }

@@ -198,12 +198,25 @@ struct TreeParams {
   float score_scale;  // scale * k_scale
   float softcap;      // 0 = none
   float v_scale;
+  int32_t spans;  // CTAs (each takes an equal span of the batch's key blocks)
+  // Rows of items that spans cut; all null when no context can be cut. Span c owns slots 2 c (its first
+  // item, begun in an earlier span) and 2 c + 1 (its last, ended in a later one).
+  float* ws_acc;     // [2 spans][D / 4][128 rows][4]
+  float2* ws_ml;     // [2 spans][128]: running maximum (log2 units) and sum
+  int32_t* ws_desc;  // [spans][kTreeDescInts]: q row, tile, KV head, rows and parts of the item begun there
   uint32_t* err;
 };
 constexpr int kTreeMaxNodes = 256;
 constexpr int kTreeMaskWords = kTreeMaxNodes / 64;
+constexpr int kTreeMaxSpans = 2 * 148;  // two CTAs per SM
+constexpr int kTreeDescInts = 8;
+constexpr int kTreeRows = 128;
 bool tree_supported(KvType kv, int head_dim, int group);
+bool tree_splits(int64_t max_context_len);  // whether a context of that length may be cut
+int tree_spans(int64_t num_seqs, int num_kv_heads, int group, int max_query_len, int64_t max_context_len);
 cudaError_t launch_decode_tree(KvType kv, QType q, int head_dim, const TreeParams& p, cudaStream_t stream);
+cudaError_t launch_decode_tree_tc(KvType kv, int head_dim, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                                  const TreeParams& p, cudaStream_t stream);
 
 // Accepted path of each sequence's tree moved to the front of its drafted region (tree_commit.cu).
 struct CommitParams {

@@ -72,10 +72,6 @@ cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t st) {
 
 }  // namespace
 
-bool tree_supported(KvType kv, int head_dim, int group) {
-  return group >= 1 && group <= 16 && (head_dim == 128 || (head_dim == 64 && kv != KvType::E4M3));
-}
-
 cudaError_t launch_decode_tree(KvType kv, QType q, int head_dim, const TreeParams& p, cudaStream_t st) {
   if (kv == KvType::E4M3)
     return q == QType::BF16 ? launch_tree_t<KvType::E4M3, true, 128>(p, st) : launch_tree_t<KvType::E4M3, false, 128>(p, st);

@@ -169,6 +169,22 @@ def test_tree_option_refusals_and_empty_calls():
 
 
 @cpu_only
+def test_tree_workspace():
+    """A table wide enough for split contexts needs the workspace that the sizing call names, 256-byte aligned."""
+    need = pa.pa_decode_tree_workspace_bytes(2, 4, 2, 128, 5, 16 * 4096)
+    assert need > 0 and need % 256 == 0
+    assert pa.pa_decode_tree_workspace_bytes(2, 4, 2, 128, 5, 64) == 0  # one key block: nothing to split
+    assert pa.pa_decode_tree_workspace_bytes(0, 4, 2, 128, 5, 4096) == 0
+    a = tree_args(bt=aligned_zeros((2, 4096), I32))
+    ws = aligned_zeros((need + 256,), torch.uint8)
+    assert attend(a) == pa.PA_ERR_WORKSPACE
+    assert attend(a, workspace=ws.data_ptr(), workspace_bytes=need - 1) == pa.PA_ERR_WORKSPACE
+    assert attend(a, workspace=ws.data_ptr() + 128, workspace_bytes=need) == INVALID
+    assert attend(a, workspace=ws.data_ptr(), workspace_bytes=need) == pa.PA_ERR_CUDA
+    assert attend(a, max_context_len=64) == pa.PA_ERR_CUDA
+
+
+@cpu_only
 @pytest.mark.parametrize("change,status,said", [
     ({"k_cache": None}, INVALID, "k_cache is NULL"),
     ({"k_cache": aligned_zeros((8, 2, 16, 128), F32), "v_cache": aligned_zeros((8, 2, 16, 128), F32)}, INVALID, "dtype"),
