@@ -1108,7 +1108,6 @@ int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache,
   p.q_stride_h = q->stride[1];
   p.o_stride_t = out->stride[0];
   p.o_stride_h = out->stride[1];
-  p.k_cache = k_cache->data;
   p.v_cache = v_cache->data;
   p.block_tables = static_cast<const int32_t*>(block_tables->data);
   p.bt_stride = block_tables->stride[0];
@@ -1145,14 +1144,9 @@ int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache,
   if (take_injected_failure()) return fail(PA_ERR_CUDA, "injected launch failure (pa_debug_fail_next_launches)");
   p.err = opts.error_word ? reinterpret_cast<uint32_t*>(opts.error_word) : library_error_word();
   if (!p.err) return fail(PA_ERR_CUDA, "no device error word (no current CUDA device?)");
-  cudaError_t e;
-  if (kv == pa::KvType::E4M3) {
-    e = pa::launch_decode_tree(kv, qt, static_cast<int>(D), p, static_cast<cudaStream_t>(stream));
-  } else {
-    CUtensorMap km, vm;
-    if ((st = encode_pool_map(&km, k_cache, elem_bytes(cd))) || (st = encode_pool_map(&vm, v_cache, elem_bytes(cd)))) return st;
-    e = pa::launch_decode_tree_tc(kv, static_cast<int>(D), km, vm, p, static_cast<cudaStream_t>(stream));
-  }
+  CUtensorMap km, vm;
+  if ((st = encode_pool_map(&km, k_cache, elem_bytes(cd))) || (st = encode_pool_map(&vm, v_cache, elem_bytes(cd)))) return st;
+  cudaError_t e = pa::launch_decode_tree(kv, qt, static_cast<int>(D), km, vm, p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(PA_ERR_CUDA, "decode_tree launch: %s", cudaGetErrorString(e));
   return ok();
 }

@@ -182,7 +182,6 @@ struct TreeParams {
   void* out;  // [T, Hq, D]
   const void* q;
   int64_t q_stride_t, q_stride_h, o_stride_t, o_stride_h;
-  const void* k_cache;
   const void* v_cache;
   const int32_t* block_tables;
   int64_t bt_stride;
@@ -214,9 +213,8 @@ constexpr int kTreeRows = 128;
 bool tree_supported(KvType kv, int head_dim, int group);
 bool tree_splits(int64_t max_context_len);  // whether a context of that length may be cut
 int tree_spans(int64_t num_seqs, int num_kv_heads, int group, int max_query_len, int64_t max_context_len);
-cudaError_t launch_decode_tree(KvType kv, QType q, int head_dim, const TreeParams& p, cudaStream_t stream);
-cudaError_t launch_decode_tree_tc(KvType kv, int head_dim, const CUtensorMap& k_map, const CUtensorMap& v_map,
-                                  const TreeParams& p, cudaStream_t stream);
+cudaError_t launch_decode_tree(KvType kv, QType q, int head_dim, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                               const TreeParams& p, cudaStream_t stream);
 
 // Accepted path of each sequence's tree moved to the front of its drafted region (tree_commit.cu).
 struct CommitParams {

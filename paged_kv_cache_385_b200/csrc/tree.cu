@@ -1,83 +1,994 @@
-// Attention of drafted nodes over the paged context for sm_100a: one warp per (node, query head), one
-// key at a time with an online softmax.
+// Attention of drafted nodes over the paged context for sm_100a, on the 5th-generation tensor cores.
+//
+// Mathematics. Row R = node * G + g of (sequence, KV head) sees the context's first `start` tokens and
+// the nodes of its sequence that its mask names; out = softmax(scale q K^T) V over them, one pass over
+// the keys with a running maximum and sum. A mask touches only the keys past `start`, at most five key
+// blocks at the end of a context: every other block is a dense product.
+//
+// Work. An item is a tile of up to 128 rows of one (sequence, KV head); 64 keys (4 pages) are a block.
+// The batch's items, laid end to end with kItemCost blocks' worth of fixed cost before each, are cut
+// into gridDim.x equal spans, so every CTA streams the same number of blocks whatever the lengths are:
+// a span's first and last items may be parts of items, whose unnormalised rows go to the workspace and
+// are joined by merge_kernel. Items of at most kWhole blocks are never cut. The cuts depend on lengths
+// alone, and partial rows are joined in span order, so results do not depend on timing or placement.
+//
+// Per block, as in the prefill kernel: S = Q K^T (tcgen05, K-major operands in 128-byte-swizzled shared
+// memory, two S buffers in tensor memory), softmax by 4 warps with a row per thread, P over S in tensor
+// memory, O += P V (A from tensor memory). Warps: 0-3 softmax, Q loads and epilogue; 4 TMA producer of K;
+// 5 QK issuer and owner of the tensor memory; 6 TMA producer of V; 7 PV issuer. e4m3 pages land as they
+// are and two more pairs of warps widen them (8-9 K, 10-11 V) into the f16 operand tiles. Two CTAs per SM.
+#include <algorithm>
+
 #include "internal.h"
 #include "pa_device.cuh"
+#include "tc05.cuh"
 
 namespace pa {
 namespace {
 
-template <KvType KV, bool kQBf16, int D>
-__global__ void __launch_bounds__(32) tree_kernel(const TreeParams p) {
-  constexpr int E = D / 32;
-  const int i = blockIdx.x, h = blockIdx.y, s = blockIdx.z, lane = threadIdx.x;
-  const int q0 = p.query_start[s], n = p.query_start[s + 1] - q0, ctx = p.context_lens[s];
-  if (n < 0 || n > p.max_query_len || n > ctx || ctx > p.max_context_len || q0 < 0 || q0 > p.num_tokens - n) {
-    if (lane == 0) atomicOr(p.err, 8u);
+constexpr int kRows = 128;  // query rows of an item
+constexpr int kKeys = 64;   // keys of a block
+constexpr int kItemCost = 2;
+constexpr int kWhole = 4;
+constexpr int kMinSpan = 6;
+constexpr uint32_t kQHalf = kRows * 128;  // a 64-element (128-byte) column half of the Q tile
+constexpr uint32_t kHalf = kKeys * 128;   // of a K or V tile
+// O is rescaled only when a row's maximum grows by more than this (log2 units): until then P and the
+// sum keep the older reference, and P stays below 2^8.
+constexpr float kLazyRescale = 8.f;
+
+constexpr uint32_t kBarBytes = 640;  // barriers and what the roles hand each other
+
+template <KvType KV, int D, bool kCap>
+struct Layout {
+  static constexpr bool kBf16 = KV == KvType::BF16;  // operand type (e4m3 pages are widened to f16)
+  static constexpr bool kFp8 = KV == KvType::E4M3;
+  static constexpr int kHalves = D / 64;
+  static constexpr uint32_t kQTile = kHalves * kQHalf;
+  static constexpr uint32_t kTile = kHalves * kHalf;
+  static constexpr int kKStages = kFp8 ? 2 : (D == 128 ? 3 : 4), kVStages = kFp8 ? 1 : (D == 128 ? 2 : 4);
+  // e4m3: pages land in rings of their own and are widened into the operand tiles.
+  static constexpr uint32_t kRawTile = kFp8 ? kHalf : 0;
+  static constexpr int kRawStages = 2;
+  static constexpr uint32_t kQOff = 0;
+  static constexpr uint32_t kKOff = kQTile;
+  static constexpr uint32_t kVOff = kKOff + kKStages * kTile;
+  static constexpr uint32_t kRawKOff = kVOff + kVStages * kTile;
+  static constexpr uint32_t kRawVOff = kRawKOff + kRawStages * kRawTile;
+  static constexpr uint32_t kBarOff = kRawVOff + kRawStages * kRawTile;
+  static constexpr uint32_t kSmemBytes = kBarOff + kBarBytes;
+  static constexpr int kThreads = kFp8 ? 384 : 256;
+  // Scores of a row that its thread holds at a time: all 64 of a block, or, where registers do not
+  // suffice (768 threads an SM, or the cap's arithmetic), 32 that are read twice from tensor memory.
+  static constexpr int kHeld = kFp8 || kCap ? 32 : 64;
+  // P is 2^(s - m + kShift): f16 keeps 7 more binades of small weights before it rounds them away
+  // (2^(8 + 7) is still finite); bf16 has float32's range.
+  static constexpr float kShift = kBf16 ? 0.f : 7.f;
+};
+constexpr uint32_t kTmemCols = 256;  // two S buffers of kKeys columns, then O's D columns
+
+// A CTA's part of an item, as the K producer hands it to the other roles through shared memory.
+struct alignas(16) Part {
+  int s, q0, rows, tile;
+  int hk, start, ctx;
+  int j0, j1;       // its key blocks; none: the span is done
+  int first, last;  // the CTAs that hold the item's first and last blocks
+  int unused;
+};
+constexpr int kParts = 4;  // parts handed on and not yet left by every role
+
+enum {
+  kQFull = 0,    // 4 softmax warps: the item's Q tile is in place
+  kKFull0 = 1,   // up to 4
+  kKEmpty0 = 5,  // up to 4
+  kVFull0 = 9,
+  kVEmpty0 = 13,
+  kSFull0 = 17,  // 2
+  kPFull0 = 19,  // 2: block gb arrives on kPFull0 + (gb & 1)
+  kODone0 = 21,  // 2: P(gb).V commits to kODone0 + (gb & 1)
+  kAllDone = 23,
+  kOFree = 24,   // the epilogue has read O (4 softmax warps)
+  kMeet = 25,    // the softmax warps meet (4)
+  kTmemSlot = 26,
+  kBadNodes = 27,  // 256 bits: nodes whose V row holds infinities or NaN
+  kRawKFull0 = 31,  // 2 each: e4m3 pages landed, and widened (2 warps)
+  kRawKEmpty0 = 33,
+  kRawVFull0 = 35,
+  kRawVEmpty0 = 37,
+  kPartFull0 = 39,   // kParts: a part is written (the K producer)
+  kPartEmpty0 = 43,  // kParts: every role has left it
+  kPart0 = 48,       // kParts parts
+};
+static_assert(kPartFull0 + kParts <= kPartEmpty0 && kPartEmpty0 + kParts <= kPart0, "barrier slots");
+static_assert(sizeof(Part) == 48 && 8 * kPart0 % 16 == 0 && 8 * kPart0 + kParts * sizeof(Part) <= kBarBytes, "barrier area");
+
+// ---- the schedule -------------------------------------------------------------------------------
+
+struct Seq {
+  int q0, n, ctx, rows, tiles, nkb;
+};
+
+// Sequence s, with no tiles when it has no nodes or is out of contract (*bad).
+__device__ __forceinline__ Seq load_seq(const TreeParams& p, int s, bool* bad) {
+  Seq q;
+  q.q0 = p.query_start[s];
+  const int64_t n = static_cast<int64_t>(p.query_start[s + 1]) - q.q0;
+  q.ctx = p.context_lens[s];
+  *bad = n < 0 || n > p.max_query_len || n > q.ctx || q.ctx > p.max_context_len || q.q0 < 0 || q.q0 > p.num_tokens - n;
+  q.n = *bad ? 0 : static_cast<int>(n);
+  q.rows = q.n * p.group;
+  q.tiles = (q.rows + kRows - 1) / kRows;
+  q.nkb = q.n ? (q.ctx + kKeys - 1) / kKeys : 0;
+  return q;
+}
+
+__device__ __forceinline__ int64_t seq_cost(const TreeParams& p, const Seq& q) {
+  return static_cast<int64_t>(q.tiles) * p.num_kv_heads * (q.nkb + kItemCost);
+}
+
+// Walks a CTA's span [beg, end) of the items laid end to end.
+struct Cursor {
+  int64_t beg, end, len;  // span, and the spans' common length
+  int64_t at;             // cost before the current item
+  int s, hk, tile;
+  Seq q;
+
+  __device__ __forceinline__ void skip_empty(const TreeParams& p) {
+    bool bad;
+    while (s < p.num_seqs && (q = load_seq(p, s, &bad)).tiles == 0) ++s;
+  }
+  __device__ __forceinline__ bool next(const TreeParams& p, Part* part) {
+    while (s < p.num_seqs && at < end) {
+      const int cost = q.nkb + kItemCost;
+      int64_t j0 = beg - at - kItemCost, j1 = end - at - kItemCost;  // the span, in this item's blocks
+      int first, last;
+      if (q.nkb <= kWhole) {  // whole, where its first block lies
+        const bool mine = j0 <= 0 && j1 > 0;
+        j0 = 0;
+        j1 = mine ? q.nkb : 0;
+        first = last = blockIdx.x;
+      } else {
+        j0 = max(j0, static_cast<int64_t>(0));
+        j1 = min(j1, static_cast<int64_t>(q.nkb));
+        first = static_cast<int>((at + kItemCost) / len);
+        last = static_cast<int>((at + cost - 1) / len);
+      }
+      if (j0 < j1) {
+        part->s = s, part->q0 = q.q0, part->rows = q.rows, part->tile = tile;
+        part->hk = hk, part->start = q.ctx - q.n, part->ctx = q.ctx;
+        part->j0 = static_cast<int>(j0), part->j1 = static_cast<int>(j1);
+        part->first = first, part->last = last;
+      }
+      at += cost;
+      if (++tile == q.tiles) {
+        tile = 0;
+        if (++hk == p.num_kv_heads) {
+          hk = 0;
+          ++s;
+          skip_empty(p);
+        }
+      }
+      if (j0 < j1) return true;
+    }
+    part->j0 = part->j1 = 0;
+    return false;
+  }
+};
+
+// The keys of block t0 .. t0 + 63 that a node sees, as bits.
+__device__ __forceinline__ uint64_t low_ones(int n) { return n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1); }
+__device__ __forceinline__ uint64_t visible_bits(const TreeParams& p, const volatile Part* P, int node, int t0) {
+  uint64_t v;
+  if (!p.mask) {
+    v = low_ones(P->start + node + 1 - t0);
+  } else {
+    const uint64_t* row = p.mask + static_cast<int64_t>(P->q0 + node) * p.mask_words;
+    const int o = t0 - P->start;
+    if (o < 0) {
+      v = low_ones(-o) | (o > -64 ? row[0] << -o : 0ull);
+    } else {
+      const int w = o >> 6, sh = o & 63;
+      v = w < p.mask_words ? row[w] >> sh : 0ull;
+      if (sh && w + 1 < p.mask_words) v |= row[w + 1] << (64 - sh);
+    }
+  }
+  return v & low_ones(P->ctx - t0);
+}
+
+// Max (kMax) or min of n values in four independent chains.
+template <bool kMax, int n>
+__device__ __forceinline__ float extreme(const float (&v)[n]) {
+  float e[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int k = 4; k < n; ++k) e[k & 3] = kMax ? fmaxf(e[k & 3], v[k]) : fminf(e[k & 3], v[k]);
+  return kMax ? fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) : fminf(fminf(e[0], e[1]), fminf(e[2], e[3]));
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// R / G for R < 4096 and G <= 16, by a multiplication: inv_g = ceil(65536 / G).
+__device__ __forceinline__ int div_group(int R, uint32_t inv_g) { return static_cast<int>((R * inv_g) >> 16); }
+
+template <KvType KV, bool kQBf16, int D, bool kCap>
+__global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
+    tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const TreeParams p) {
+  using L = Layout<KV, D, kCap>;
+  constexpr bool kBf16 = L::kBf16;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t base = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (base & 1023u) {  // the swizzled tiles need 1024-byte alignment; never seen, but do not guess
+    if (threadIdx.x == 0) atomicOr(p.err, 4u);
     return;
   }
-  if (i >= n) return;
-  const int hk = h / p.group, start = ctx - n;
-  const uint16_t* qr = static_cast<const uint16_t*>(p.q) + (q0 + i) * p.q_stride_t + h * p.q_stride_h;
-  float q[E], o[E];
-  for (int e = 0; e < E; ++e) {
-    q[e] = unpack2<kQBf16>(qr[lane + 32 * e]).x;
-    o[e] = 0.f;
+  const uint32_t bar = base + L::kBarOff;
+  auto B = [&](int i) { return bar + 8u * i; };
+  pdl_wait();
+
+  // ---- this CTA's span: cost before each thread's share of the sequences ------------------------
+  Cursor cur;
+  {
+    constexpr int T = L::kThreads;
+    int64_t* before = reinterpret_cast<int64_t*>(smem);  // [T + 1], in the ring before it is used
+    const int per = (p.num_seqs + T - 1) / T;
+    const int s0 = min(static_cast<int>(threadIdx.x) * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
+    int64_t mine = 0;
+    bool any_bad = false;
+    for (int s = s0; s < s1; ++s) {
+      bool bad;
+      mine += seq_cost(p, load_seq(p, s, &bad));
+      any_bad |= bad;
+    }
+    if (any_bad && blockIdx.x == 0) atomicOr(p.err, 8u);
+    int64_t incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t v = __shfl_up_sync(kFull, incl, off);
+      if (lane >= off) incl += v;
+    }
+    int64_t* totals = before + T + 1;  // one per warp
+    if (lane == 31) totals[warp] = incl;
+    __syncthreads();
+    int64_t base_cost = 0;
+    for (int w = 0; w < warp; ++w) base_cost += totals[w];
+    before[threadIdx.x] = base_cost + incl - mine;
+    if (threadIdx.x == T - 1) before[T] = base_cost + incl;
+    __syncthreads();
+    const int64_t total = before[T];
+    cur.len = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinSpan));
+    cur.beg = cur.len * blockIdx.x;
+    cur.end = min(cur.beg + cur.len, total);
+    if (cur.beg >= total) {
+      if (threadIdx.x == 0 && p.ws_desc) p.ws_desc[blockIdx.x * kTreeDescInts + 4] = 0;
+      return;
+    }
+    int lo = 0, hi = T - 1;  // the last share that starts at or before the span
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (before[mid] <= cur.beg) lo = mid;
+      else hi = mid - 1;
+    }
+    cur.at = before[lo];
+    cur.s = min(lo * per, p.num_seqs);
+    cur.hk = cur.tile = 0;
+    cur.skip_empty(p);
+    while (cur.s < p.num_seqs && cur.at + seq_cost(p, cur.q) <= cur.beg) {
+      cur.at += seq_cost(p, cur.q);
+      ++cur.s;
+      cur.skip_empty(p);
+    }
+    // The item of that sequence in which the span begins.
+    const int cost = cur.q.nkb + kItemCost;
+    const int item = static_cast<int>((cur.beg - cur.at) / cost);
+    cur.at += static_cast<int64_t>(item) * cost;
+    cur.hk = item / cur.q.tiles;
+    cur.tile = item % cur.q.tiles;
   }
-  float m = -INFINITY, l = 0.f;
-  for (int t = 0; t < ctx; ++t) {
-    const int j = t - start;
-    bool seen = j < 0;
-    if (j >= 0) seen = p.mask ? (p.mask[(int64_t)(q0 + i) * p.mask_words + j / 64] >> (j % 64)) & 1 : j <= i;
-    if (!seen) continue;
-    const int b = p.block_tables[s * p.bt_stride + t / 16];
-    if (b < 0 || b >= p.num_blocks) {
-      if (lane == 0) atomicOr(p.err, 1u);
-      continue;
+  __syncthreads();  // the shares are read: the ring may be written
+
+  if (threadIdx.x == 0) {
+    mbar_init(B(kQFull), 4);
+    for (int i = 0; i < L::kKStages; ++i) {
+      mbar_init(B(kKFull0 + i), L::kFp8 ? 2 : 1);
+      mbar_init(B(kKEmpty0 + i), 1);
     }
-    const int64_t at = ((int64_t)(b * p.num_kv_heads + hk) * 16 + t % 16) * D;
-    float k[E], v[E], x = 0.f;
-    for (int e = 0; e < E; ++e) {
-      const int64_t a = at + lane + 32 * e;
-      if constexpr (KV == KvType::E4M3) {
-        __nv_fp8_e4m3 f;
-        f.__x = static_cast<const uint8_t*>(p.k_cache)[a];
-        k[e] = static_cast<float>(f);
-        f.__x = static_cast<const uint8_t*>(p.v_cache)[a];
-        v[e] = static_cast<float>(f);
-      } else {
-        k[e] = unpack2<KV == KvType::BF16>(static_cast<const uint16_t*>(p.k_cache)[a]).x;
-        v[e] = unpack2<KV == KvType::BF16>(static_cast<const uint16_t*>(p.v_cache)[a]).x;
+    for (int i = 0; i < L::kVStages; ++i) {
+      mbar_init(B(kVFull0 + i), L::kFp8 ? 2 : 1);
+      mbar_init(B(kVEmpty0 + i), 1);
+    }
+    if constexpr (L::kFp8) {
+      for (int i = 0; i < L::kRawStages; ++i) {
+        mbar_init(B(kRawKFull0 + i), 1);
+        mbar_init(B(kRawKEmpty0 + i), 2);
+        mbar_init(B(kRawVFull0 + i), 1);
+        mbar_init(B(kRawVEmpty0 + i), 2);
       }
-      x += q[e] * k[e];
     }
-    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(kFull, x, off);
-    x *= p.score_scale;
-    if (p.softcap > 0.f) x = p.softcap * tanhf(x / p.softcap);
-    const float mn = fmaxf(m, x), al = m == -INFINITY ? 0.f : expf(m - mn), w = expf(x - mn);
-    l = l * al + w;
-    for (int e = 0; e < E; ++e) o[e] = o[e] * al + w * v[e];
-    m = mn;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(B(kSFull0 + i), 1);
+      mbar_init(B(kPFull0 + i), 4);
+      mbar_init(B(kODone0 + i), 1);
+    }
+    for (int i = 0; i < kParts; ++i) {
+      mbar_init(B(kPartFull0 + i), 1);
+      mbar_init(B(kPartEmpty0 + i), L::kFp8 ? 11 : 7);  // V producer, issuers, 4 softmax warps, 4 widening ones
+    }
+    mbar_init(B(kOFree), 4);
+    mbar_init(B(kMeet), 4);
+    mbar_init(B(kAllDone), 1);
+    fence_barrier_init();
+  }
+  if (warp == 5) tc05::alloc(B(kTmemSlot), kTmemCols);
+  tc05::fence_before_sync();
+  __syncthreads();
+  tc05::fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kBarOff + 8 * kTmemSlot);
+  const uint32_t tS0 = tmem, tO = tmem + 2 * kKeys;
+  bool ok = true;
+  int issued = 0;  // producer lanes: fills issued (for the drain after a failure)
+  constexpr uint64_t kWaitNs = 2000000000ull;
+
+  // The K producer walks the span and hands on its parts; every role takes the same parts and blocks. g
+  // counts the blocks of the CTA's earlier parts (the rings' and buffers' phases run on across parts)
+  // and it the parts.
+  volatile Part* parts = reinterpret_cast<volatile Part*>(smem + L::kBarOff + 8 * kPart0);
+  auto take_part = [&](int it, uint64_t deadline) -> volatile Part* {
+    if (!mbar_wait_bounded(B(kPartFull0 + it % kParts), (it / kParts) & 1, deadline)) return nullptr;
+    return parts + it % kParts;
+  };
+  auto leave_part = [&](int it) { mbar_arrive(B(kPartEmpty0 + it % kParts)); };
+  // The part's pages of blocks j0 .. j1 - 1 into a ring of ns stages.
+  auto produce = [&](const volatile Part* P, int g, const CUtensorMap* map, uint32_t off, int ns, int full0, int empty0,
+                     uint64_t deadline) -> bool {
+    constexpr int kPages = kKeys / 16;
+    const int oob_row = p.num_blocks * p.num_kv_heads * 16;  // a box starting here is all zero fill
+    const int npages = (P->ctx + 15) / 16, hk = P->hk, j1 = P->j1;
+    const int32_t* bt = p.block_tables + static_cast<int64_t>(P->s) * p.bt_stride;
+    int ids[kPages];  // the block's page ids, loaded a block ahead
+    auto fetch = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < kPages; ++i) ids[i] = j < j1 && j * kPages + i < npages ? bt[j * kPages + i] : -1;
+    };
+    fetch(P->j0);
+    for (int j = P->j0; j < j1; ++j, ++g) {
+      int ys[kPages];
+#pragma unroll
+      for (int i = 0; i < kPages; ++i) {
+        ys[i] = oob_row;
+        if (ids[i] >= 0 && ids[i] < p.num_blocks) ys[i] = (ids[i] * p.num_kv_heads + hk) * 16;
+        else if (j * kPages + i < npages) atomicOr(p.err, 1u);
+      }
+      fetch(j + 1);
+      const int st = g % ns;
+      if (g >= ns && !mbar_wait_bounded(B(empty0 + st), ((g / ns) - 1) & 1, deadline)) return false;
+      constexpr uint32_t kBytes = L::kFp8 ? L::kRawTile : L::kTile;  // 128-byte rows, one or two per key
+      const uint32_t dst = base + off + st * kBytes;
+      mbar_arrive_expect_tx(B(full0 + st), kBytes);
+#pragma unroll
+      for (int i = 0; i < kPages; ++i)
+#pragma unroll
+        for (uint32_t u = 0; u < kBytes / kHalf; ++u)
+          tma_load_2d(dst + u * kHalf + i * 2048, map, B(full0 + st), u * 64, ys[i]);
+      ++issued;
+    }
+    return true;
+  };
+
+  // e4m3: two warps widen one ring's pages into its operand tiles, exactly (every code is an f16).
+  auto widen_all = [&](uint32_t raw_off, int raw_full0, int raw_empty0, uint32_t off, int ns, int full0, int empty0) {
+    const int t = threadIdx.x & 63;
+    for (int it = 0, g = 0;; ++it) {
+      const uint64_t deadline = globaltimer_ns() + kWaitNs;
+      const volatile Part* P = take_part(it, deadline);
+      ok = __all_sync(kFull, P != nullptr);
+      if (!ok) break;
+      const int blocks = P->j1 - P->j0;
+      __syncwarp();
+      if (lane == 0) leave_part(it);
+      if (blocks == 0) break;
+      for (int j = 0; j < blocks; ++j, ++g) {
+        const int rs = g % L::kRawStages, st = g % ns;
+        const bool got = mbar_wait_bounded(B(raw_full0 + rs), (g / L::kRawStages) & 1, deadline) &&
+                         (g < ns || mbar_wait_bounded(B(empty0 + st), ((g / ns) - 1) & 1, deadline));
+        if (!__all_sync(kFull, got)) {
+          ok = false;
+          break;
+        }
+        const uint32_t raw = base + raw_off + rs * kHalf, dst = base + off + st * L::kTile;
+#pragma unroll 4
+        for (int i = 0; i < 8; ++i) {
+          const int row = (t >> 3) + 8 * i, c = t & 7;  // 16 codes; 8 lanes read a row's 128 bytes
+          uint32_t w[4], o[8];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(raw + row * 128 + ((c ^ (row & 7)) << 4)));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2x2(w[k], o[2 * k], o[2 * k + 1]);
+          // Chunks 2c and 2c + 1 of the widened row. Lanes of the second half take the odd one first, so
+          // that the eight lanes of a row never meet on a bank.
+          const uint32_t line = dst + (c >> 2) * kHalf + row * 128;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int odd = h ^ (c >> 2), e = (2 * c + odd) & 7;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + ((e ^ (row & 7)) << 4)),
+                         "r"(odd ? o[4] : o[0]), "r"(odd ? o[5] : o[1]), "r"(odd ? o[6] : o[2]), "r"(odd ? o[7] : o[3])
+                         : "memory");
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(B(full0 + st));
+          mbar_arrive(B(raw_empty0 + rs));
+        }
+      }
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) atomicOr(p.err, 4u);
+  };
+
+  if (warp >= 8) {
+    if constexpr (L::kFp8) {
+      if (warp < 10) widen_all(L::kRawKOff, kRawKFull0, kRawKEmpty0, L::kKOff, L::kKStages, kKFull0, kKEmpty0);
+      else widen_all(L::kRawVOff, kRawVFull0, kRawVEmpty0, L::kVOff, L::kVStages, kVFull0, kVEmpty0);
+    }
+  } else if (warp == 4) {
+    // ---- TMA producer of K, and the schedule ---------------------------------------------------------
+    if (lane == 0) {
+      prefetch_tensormap(&kmap);
+      for (int it = 0, g = 0; ok; ++it) {
+        const uint64_t deadline = globaltimer_ns() + kWaitNs;
+        Part P;
+        const bool more = cur.next(p, &P);
+        if (it >= kParts && !mbar_wait_bounded(B(kPartEmpty0 + it % kParts), (it / kParts - 1) & 1, deadline)) {
+          ok = false;
+          break;
+        }
+        volatile Part* to = parts + it % kParts;
+        to->s = P.s, to->q0 = P.q0, to->rows = P.rows, to->tile = P.tile, to->hk = P.hk, to->start = P.start;
+        to->ctx = P.ctx, to->j0 = P.j0, to->j1 = P.j1, to->first = P.first, to->last = P.last;
+        mbar_arrive(B(kPartFull0 + it % kParts));
+        if (!more) break;
+        if constexpr (L::kFp8) ok = produce(&P, g, &kmap, L::kRawKOff, L::kRawStages, kRawKFull0, kRawKEmpty0, deadline);
+        else ok = produce(&P, g, &kmap, L::kKOff, L::kKStages, kKFull0, kKEmpty0, deadline);
+        g += P.j1 - P.j0;
+      }
+      if (!ok) atomicOr(p.err, 4u);
+    }
+  } else if (warp == 6) {
+    // ---- TMA producer of V ---------------------------------------------------------------------------
+    if (lane == 0) {
+      prefetch_tensormap(&vmap);
+      for (int it = 0, g = 0; ok; ++it) {
+        const uint64_t deadline = globaltimer_ns() + kWaitNs;
+        const volatile Part* P = take_part(it, deadline);
+        ok = P != nullptr;
+        if (!ok || P->j0 == P->j1) break;
+        if constexpr (L::kFp8) ok = produce(P, g, &vmap, L::kRawVOff, L::kRawStages, kRawVFull0, kRawVEmpty0, deadline);
+        else ok = produce(P, g, &vmap, L::kVOff, L::kVStages, kVFull0, kVEmpty0, deadline);
+        g += P->j1 - P->j0;
+        leave_part(it);
+      }
+      if (!ok) atomicOr(p.err, 4u);
+    }
+  } else if (warp == 5) {
+    // ---- QK issuer: S(g) = Q K(g)^T into S buffer g & 1 ----------------------------------------------
+    if (lane == 0) {
+      constexpr uint32_t idesc = tc05::idesc_f16(kBf16, kRows, kKeys, false, false);
+      for (int it = 0, g = 0; ok; ++it) {
+        const uint64_t deadline = globaltimer_ns() + kWaitNs;
+        const volatile Part* P = take_part(it, deadline);
+        ok = P != nullptr;
+        if (!ok) break;
+        const int blocks = P->j1 - P->j0;
+        leave_part(it);
+        if (blocks == 0) break;
+        ok = mbar_wait_bounded(B(kQFull), it & 1, deadline);
+        for (int j = 0; j < blocks && ok; ++j, ++g) {
+          // Buffer g & 1 holds P(g - 2) until P(g - 2).V has run. O_done is two barriers by parity: the
+          // one waited for here next completes for P(g).V, which needs the S issued below.
+          const int st = g % L::kKStages;
+          if ((g >= 2 && !mbar_wait_bounded(B(kODone0 + (g & 1)), ((g - 2) >> 1) & 1, deadline)) ||
+              !mbar_wait_bounded(B(kKFull0 + st), (g / L::kKStages) & 1, deadline)) {
+            ok = false;
+            break;
+          }
+          tc05::fence_after_sync();
+          const uint32_t kb = base + L::kKOff + st * L::kTile;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t cb = (ks & 3) * 32;
+            tc05::mma_f16(tS0 + (g & 1) * kKeys, tc05::smem_desc_sw128(base + L::kQOff + (ks >> 2) * kQHalf + cb, 16, 1024),
+                          tc05::smem_desc_sw128(kb + (ks >> 2) * kHalf + cb, 16, 1024), idesc, ks > 0);
+          }
+          tc05::commit(B(kSFull0 + (g & 1)));
+          tc05::commit(B(kKEmpty0 + st));
+        }
+      }
+      if (!ok) atomicOr(p.err, 4u);
+    }
+  } else if (warp == 7) {
+    // ---- PV issuer: O += P(g) V(g) ---------------------------------------------------------------------
+    if (lane == 0) {
+      constexpr uint32_t idesc = tc05::idesc_f16(kBf16, kRows, D, false, true);
+      for (int it = 0, g = 0; ok; ++it) {
+        const uint64_t deadline = globaltimer_ns() + kWaitNs;
+        const volatile Part* P = take_part(it, deadline);
+        ok = P != nullptr;
+        if (!ok) break;
+        const int blocks = P->j1 - P->j0;
+        leave_part(it);
+        if (blocks == 0) break;
+        // The part's first product overwrites O: the epilogue before it must have read it.
+        if (it > 0) ok = mbar_wait_bounded(B(kOFree), (it - 1) & 1, deadline);
+        for (int j = 0; j < blocks && ok; ++j, ++g) {
+          const int st = g % L::kVStages;
+          if (!mbar_wait_bounded(B(kPFull0 + (g & 1)), (g >> 1) & 1, deadline) ||
+              !mbar_wait_bounded(B(kVFull0 + st), (g / L::kVStages) & 1, deadline)) {
+            ok = false;
+            break;
+          }
+          tc05::fence_after_sync();
+          const uint32_t vb = base + L::kVOff + st * L::kTile;
+#pragma unroll
+          for (int kt = 0; kt < kKeys / 16; ++kt)
+            tc05::mma_f16_ts(tO, tS0 + (g & 1) * kKeys + kt * 8, tc05::smem_desc_sw128(vb + kt * 2048, kHalf, 1024), idesc,
+                             j > 0 || kt > 0);
+          tc05::commit(B(kODone0 + (g & 1)));
+          tc05::commit(B(kVEmpty0 + st));
+        }
+      }
+      // Every QK has completed before its softmax finished, so this covers all of the CTA's MMAs.
+      tc05::commit(B(kAllDone));
+      mbar_wait_bounded(B(kAllDone), 0, globaltimer_ns() + 1000000000ull);
+      if (!ok) atomicOr(p.err, 4u);
+    }
+  } else {
+    // ---- softmax warps: thread = row -----------------------------------------------------------------
+    const int r = threadIdx.x;  // 0..127, the row's TMEM lane
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    const int G = p.group;
+    const uint32_t inv_g = (65536u + G - 1) / G;
+    // A negative scale turns Q's sign (load_q), so that the largest product gives the largest score.
+    const bool negate = p.score_scale < 0.f;
+    const float sl2 = fabsf(p.score_scale) * 1.4426950408889634f;
+    // Capped scores: cap * tanh(s / cap) = cap - 2 cap / (1 + 2^(u s)), in log2 units.
+    const float cap2 = kCap ? p.softcap * 1.4426950408889634f : 0.f;
+    const float cap_u = kCap ? 2.f * sl2 / p.softcap : 0.f;
+    volatile uint32_t* bad_nodes = reinterpret_cast<volatile uint32_t*>(smem + L::kBarOff + 8 * kBadNodes);
+    int meets = 0;
+    if (r == 0 && p.ws_desc) p.ws_desc[blockIdx.x * kTreeDescInts + 4] = 0;
+
+    auto score = [&](float s) -> float {  // a raw product in log2 units
+      if constexpr (kCap) return fmaf(-2.f * cap2, rcp_approx(1.f + ex2(s * cap_u)), cap2);
+      else return s * sl2;
+    };
+    auto weight = [&](float s, float nref) -> float {
+      if constexpr (kCap) return ex2(score(s) + nref);
+      else return ex2(fmaf(s, sl2, nref));
+    };
+    // The four warps meet (a bounded wait: a warp that gave up does not come).
+    auto meet = [&](uint64_t deadline) -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(B(kMeet));
+      const bool got = mbar_wait_bounded(B(kMeet), meets & 1, deadline);
+      ++meets;
+      return __all_sync(kFull, got);
+    };
+    // A part's Q rows into the swizzled tile, as asynchronous copies of 16-byte chunks, a row's by
+    // neighbouring lanes; rows past the last are zero. start_q may run once the QKs of the part before
+    // have (this warp has seen its last S), finish_q hands the tile to the QK issuer.
+    constexpr int kRowChunks = D / 8;
+    auto q_addr = [&](int x) -> uint32_t {
+      const int row = warp * 32 + x / kRowChunks, c = x % kRowChunks;
+      return base + L::kQOff + (c >> 3) * kQHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+    };
+    auto start_q = [&](const volatile Part* P) {
+      const int row0 = P->tile * kRows + warp * 32, rows = P->rows, head0 = P->hk * G;
+      const uint16_t* q0 = static_cast<const uint16_t*>(p.q) + P->q0 * p.q_stride_t;
+#pragma unroll 4
+      for (int x = lane; x < 32 * kRowChunks; x += 32) {
+        const int R = row0 + x / kRowChunks, node = div_group(R, inv_g);
+        const uint16_t* src = q0;
+        uint32_t bytes = 0;
+        if (R < rows) {
+          src = q0 + node * p.q_stride_t + (head0 + R - node * G) * p.q_stride_h + x % kRowChunks * 8;
+          bytes = 16;
+        }
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_addr(x)), "l"(src), "r"(bytes) : "memory");
+      }
+    };
+    auto finish_q = [&] {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if ((kQBf16 && !kBf16) || negate) {  // this lane's own chunks: bf16 to f16, and the sign
+#pragma unroll 4
+        for (int x = lane; x < 32 * kRowChunks; x += 32) {
+          uint32_t w[4];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(q_addr(x)));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (negate) w[i] ^= 0x80008000u;
+            if constexpr (kQBf16 && !kBf16) {
+              const float2 f = unpack2<true>(w[i]);
+              w[i] = pack2<false>(f.x, f.y);
+            }
+          }
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(q_addr(x)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(B(kQFull));
+    };
+
+    for (int it = 0, g = 0; ok; ++it) {
+      const uint64_t deadline = globaltimer_ns() + kWaitNs;
+      const volatile Part* P = take_part(it, deadline);
+      ok = __all_sync(kFull, P != nullptr);
+      if (!ok) break;
+      const int j0 = P->j0, j1 = P->j1;
+      if (j0 == j1) break;
+      if (it == 0) {
+        start_q(P);
+        finish_q();
+      }
+      const int rows_left = P->rows - P->tile * kRows;
+      const bool valid = r < rows_left;
+      const bool working = warp * 32 < rows_left;  // warps past the last row only keep step
+      const int node = valid ? div_group(P->tile * kRows + r, inv_g) : 0;
+      const int j_mask = P->start / kKeys;  // the first block that holds a drafted node or the end
+      const bool had_tail = j1 > j_mask;
+      if (had_tail) {  // no warp reads the bits of the part before any more; they are cleared
+        ok = meet(deadline);
+        if (r < 8) bad_nodes[r] = 0u;
+        ok = ok && meet(deadline);
+        if (!ok) break;
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int j = j0; j < j1; ++j) {
+        const int gb = g + j - j0;
+        const bool got = mbar_wait_bounded(B(kSFull0 + (gb & 1)), (gb >> 1) & 1, deadline);
+        if (!__all_sync(kFull, got)) {
+          ok = false;
+          break;
+        }
+        tc05::fence_after_sync();
+        const int t0 = j * kKeys;
+        // The next part's Q starts on its way as soon as this part's last QK has run.
+        if (j == j1 - 1) {
+          const volatile Part* N = take_part(it + 1, deadline);
+          ok = __all_sync(kFull, N != nullptr);
+          if (!ok) break;
+          if (N->j0 < N->j1) start_q(N);
+        }
+        if (working) {
+          const uint32_t tS = tS0 + (gb & 1) * kKeys + lane_off;
+          const bool masked = j >= j_mask;
+          uint64_t vis = ~0ull;
+          if (masked) {
+            vis = valid ? visible_bits(p, P, node, t0) : 0ull;
+            __syncwarp();
+          }
+          // The block's largest score in log2 units: cap and scale are monotone, so they are applied to the
+          // largest raw score alone.
+          float sv[L::kHeld], top = -INFINITY;
+          if constexpr (L::kHeld == kKeys) tc05::ld64(tS, sv);
+#pragma unroll
+          for (int h = 0; h < kKeys / L::kHeld; ++h) {
+            if constexpr (L::kHeld == 32) tc05::ld32(tS + 32 * h, sv);
+            if (masked) {
+              const uint64_t bits = vis >> (32 * h);
+#pragma unroll
+              for (int k = 0; k < L::kHeld; ++k)
+                if (!(static_cast<uint32_t>(bits >> (k & 32)) >> (k & 31) & 1u)) sv[k] = -INFINITY;
+            }
+            top = fmaxf(top, extreme<true, L::kHeld>(sv));
+          }
+          const float mx = vis == 0ull ? -INFINITY : score(top);
+          const bool raise = __any_sync(kFull, mx > m + kLazyRescale);
+          float alpha = 1.f;
+          if (raise) {
+            const float mn = fmaxf(m, mx);
+            alpha = m == -INFINITY ? (mn == -INFINITY ? 1.f : 0.f) : ex2(m - mn);
+            m = mn;
+          }
+          const float nref = L::kShift - (m == -INFINITY ? 0.f : m);
+          float rs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < kKeys / 32; ++h) {
+            // (P of the first half lies over that half's scores: the second's are still there.)
+            if constexpr (L::kHeld == 32) tc05::ld32(tS + 32 * h, sv);
+            float* x = sv + (L::kHeld == 32 ? 0 : 32 * h);
+            uint32_t wd[16];
+            if (!masked) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                x[k] = weight(x[k], nref);
+                rs[k & 3] += x[k];
+              }
+            } else {
+              const uint32_t bits = static_cast<uint32_t>(vis >> (32 * h));
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                x[k] = bits >> k & 1u ? weight(x[k], nref) : 0.f;
+                rs[k & 3] += x[k];
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) wd[k] = pack2<kBf16>(x[2 * k], x[2 * k + 1]);
+            tc05::st16u_nowait(tS + 16 * h, wd);
+          }
+          l = l * alpha + ((rs[0] + rs[1]) + (rs[2] + rs[3]));
+          // O's rescale waits for the P.V before it. Its barrier next completes for P(gb + 1).V, which
+          // needs this warp's P(gb + 1): never two phases ahead.
+          if (raise && j > j0) {
+            const bool done = mbar_wait_bounded(B(kODone0 + ((gb - 1) & 1)), ((gb - 1) >> 1) & 1, deadline);
+            if (!__all_sync(kFull, done)) {
+              ok = false;
+              break;
+            }
+            tc05::fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              float v[32];
+              tc05::ld32(tO + lane_off + c * 32, v);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] *= alpha;
+              tc05::st32(tO + lane_off + c * 32, v);
+            }
+          }
+          tc05::st_wait();
+        }
+        // V rows of drafted nodes and behind the context. A weight of 0 must take nothing from a row that
+        // holds infinities or NaN: rows behind the context are zeroed, and a node's non-finite elements
+        // too, the node noted for the epilogue, which gives them to the rows that do see it.
+        if (j >= j_mask) {
+          const bool landed = mbar_wait_bounded(B(kVFull0 + gb % L::kVStages), (gb / L::kVStages) & 1, deadline);
+          if (!__all_sync(kFull, landed)) {
+            ok = false;
+            break;
+          }
+          constexpr int C = D / 8;
+          constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u;
+          const uint32_t vb = base + L::kVOff + (gb % L::kVStages) * L::kTile;
+          const int start = P->start, first = max(start - t0, 0), held = P->ctx - t0;
+          for (int x = r; x < (kKeys - first) * C; x += 128) {
+            const int row = first + x / C, c = x % C;
+            const uint32_t a = vb + (c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+            uint32_t w[4], odd = 0u;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t is = row < held ? __vcmpeq2(w[i] & kExp, kExp) : 0xffffffffu;
+              odd |= is;
+              w[i] &= ~is;
+            }
+            if (odd) {
+              if (row < held) {
+                const int nd = t0 + row - start;
+                atomicOr(const_cast<uint32_t*>(&bad_nodes[nd >> 5]), 1u << (nd & 31));
+              }
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                           : "memory");
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        tc05::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(B(kPFull0 + (gb & 1)));
+      }
+      if (!ok) break;
+      const int gl = g + j1 - j0 - 1;
+      g = gl + 1;
+      {
+        const volatile Part* N = parts + (it + 1) % kParts;
+        if (N->j0 < N->j1) finish_q();  // before the epilogue, which the next part's first QK overlaps
+      }
+      // ---- epilogue ------------------------------------------------------------------------------------
+      if (!__all_sync(kFull, mbar_wait_bounded(B(kODone0 + (gl & 1)), (gl >> 1) & 1, deadline)) ||
+          (had_tail && !meet(deadline))) {
+        ok = false;
+        break;
+      }
+      tc05::fence_after_sync();
+      const int first = P->first;
+      const bool whole = first == P->last;
+      const int slot = 2 * blockIdx.x + (first == static_cast<int>(blockIdx.x));
+      const float inv = l == 0.f ? 0.f : p.v_scale / l;
+      const int head = P->hk * G + P->tile * kRows + r - node * G;
+      uint16_t* dst = static_cast<uint16_t*>(p.out) + (P->q0 + node) * p.o_stride_t + head * p.o_stride_h;
+      uint32_t any_bad = 0u;
+      if (had_tail) {
+#pragma unroll
+        for (int w = 0; w < 8; ++w) any_bad |= bad_nodes[w];
+      }
+      if (working) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float v[32];
+          tc05::ld32(tO + lane_off + c * 32, v);
+          if (any_bad && valid) {  // non-finite values of nodes that this row sees
+            const int32_t* bt = p.block_tables + static_cast<int64_t>(P->s) * p.bt_stride;
+            for (int w = 0; w < 8; ++w) {
+              for (uint32_t bits = bad_nodes[w]; bits; bits &= bits - 1) {
+                const int nd = 32 * w + __ffs(bits) - 1, t = P->start + nd;
+                if (!(visible_bits(p, P, node, t) & 1ull)) continue;
+                const int64_t at = ((static_cast<int64_t>(bt[t >> 4]) * p.num_kv_heads + P->hk) * 16 + (t & 15)) * D + c * 32;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                  if constexpr (L::kFp8) {
+                    if ((static_cast<const uint8_t*>(p.v_cache)[at + k] & 0x7f) == 0x7f) v[k] = NAN;
+                  } else {
+                    const float x = unpack2<kBf16>(static_cast<const uint16_t*>(p.v_cache)[at + k]).x;
+                    if (!isfinite(x)) v[k] += x;
+                  }
+                }
+              }
+            }
+          }
+          if (valid && whole) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint4 o;
+              o.x = pack2<kQBf16>(v[8 * q] * inv, v[8 * q + 1] * inv);
+              o.y = pack2<kQBf16>(v[8 * q + 2] * inv, v[8 * q + 3] * inv);
+              o.z = pack2<kQBf16>(v[8 * q + 4] * inv, v[8 * q + 5] * inv);
+              o.w = pack2<kQBf16>(v[8 * q + 6] * inv, v[8 * q + 7] * inv);
+              *reinterpret_cast<uint4*>(dst + c * 32 + 8 * q) = o;
+            }
+          } else if (valid) {
+            // Partial rows: four columns of the tile's 128 rows together, so that a warp's stores and
+            // the merge's loads are whole lines.
+            float4* ws = reinterpret_cast<float4*>(p.ws_acc) + static_cast<int64_t>(slot) * (D / 4) * kRows + r;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              ws[(8 * c + q) * kRows] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          }
+          __syncwarp();  // the tensor-memory load above is the whole warp's
+        }
+        if (valid && !whole) p.ws_ml[slot * kRows + r] = make_float2(m, l);
+      }
+      if (r == 0 && !whole && first == static_cast<int>(blockIdx.x)) {
+        int32_t* d = p.ws_desc + blockIdx.x * kTreeDescInts;
+        d[0] = P->q0;
+        d[1] = P->tile;
+        d[2] = P->hk;
+        d[3] = P->rows;
+        d[4] = P->last - first + 1;
+      }
+      tc05::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(B(kOFree));
+        leave_part(it);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (a part that was given up may have its Q on the way)
+    if (!ok && lane == 0) atomicOr(p.err, 4u);
+  }
+  pdl_launch_dependents();
+  tc05::fence_before_sync();
+  const int any_fail = __syncthreads_or(!ok);
+  if (warp == 5) {
+    tc05::fence_after_sync();
+    tc05::dealloc(tmem, kTmemCols);
+  }
+  if (any_fail && (warp == 4 || warp == 6) && lane == 0) {
+    // A wait gave up, so copies in flight may not have been consumed: give them a bounded chance to land
+    // before the shared memory goes. Only the last fill of each stage can be outstanding.
+    const int ns = L::kFp8 ? L::kRawStages : (warp == 4 ? L::kKStages : L::kVStages);
+    const int full0 = warp == 4 ? (L::kFp8 ? kRawKFull0 : kKFull0) : (L::kFp8 ? kRawVFull0 : kVFull0);
+    const uint64_t drain_deadline = globaltimer_ns() + 100000000ull;
+    for (int j = max(0, issued - ns); j < issued; ++j)
+      mbar_wait_bounded(B(full0 + j % ns), (j / ns) & 1, drain_deadline);
+  }
+}
+
+// Joins the parts of the items that spans cut: block (c, y) takes rows 8 y .. 8 y + 7 of the item that
+// begins in span c and ends in a later one.
+template <bool kOutBf16, int D>
+__global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
+  constexpr int V = D / 64;  // float4 columns of a thread
+  pdl_wait();
+  const int c = blockIdx.x;
+  const int32_t* d = p.ws_desc + c * kTreeDescInts;
+  const int parts = d[4];
+  if (parts == 0) return;
+  const int r = blockIdx.y * 8 + (threadIdx.x & 7), col = threadIdx.x >> 3;  // columns col, col + 16 of D / 4
+  const int R = d[1] * kRows + r;
+  if (R >= d[3]) return;
+  auto slot = [&](int k) -> int64_t { return k == 0 ? 2 * c + 1 : 2 * (c + k); };
+  float top = -INFINITY;
+  for (int k = 0; k < parts; ++k) top = fmaxf(top, p.ws_ml[slot(k) * kRows + r].x);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float4 acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k) {
+    const float2 ml = p.ws_ml[slot(k) * kRows + r];
+    const float w = ex2(ml.x - ref);
+    l += w * ml.y;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float4 a = reinterpret_cast<const float4*>(p.ws_acc)[(slot(k) * (D / 4) + col + 16 * v) * kRows + r];
+      acc[v].x += w * a.x;
+      acc[v].y += w * a.y;
+      acc[v].z += w * a.z;
+      acc[v].w += w * a.w;
+    }
   }
   const float inv = l == 0.f ? 0.f : p.v_scale / l;
-  uint16_t* out = static_cast<uint16_t*>(p.out) + (q0 + i) * p.o_stride_t + h * p.o_stride_h;
-  for (int e = 0; e < E; ++e) out[lane + 32 * e] = static_cast<uint16_t>(pack2<kQBf16>(o[e] * inv, 0.f) & 0xffffu);
+  const int node = R / p.group;
+  uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(d[0] + node) * p.o_stride_t +
+                  static_cast<int64_t>(d[2] * p.group + R - node * p.group) * p.o_stride_h;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    *reinterpret_cast<uint2*>(out + 4 * (col + 16 * v)) =
+        make_uint2(pack2<kOutBf16>(acc[v].x * inv, acc[v].y * inv), pack2<kOutBf16>(acc[v].z * inv, acc[v].w * inv));
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <KvType KV, bool kQBf16, int D, bool kCap>
+cudaError_t launch_t(const CUtensorMap& km, const CUtensorMap& vm, const TreeParams& p, cudaStream_t st) {
+  using L = Layout<KV, D, kCap>;
+  auto kern = tree_kernel<KV, kQBf16, D, kCap>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(kern, dim3(p.spans), L::kThreads, L::kSmemBytes, st, km, vm, p);
+  if (e != cudaSuccess || !p.ws_desc) return e;
+  return launch_dependent(tree_merge_kernel<kQBf16, D>, dim3(p.spans, kRows / 8), 128, 0, st, p);
 }
 
 template <KvType KV, bool kQBf16, int D>
-cudaError_t launch_tree_t(const TreeParams& p, cudaStream_t st) {
-  const dim3 grid(p.max_query_len, p.num_kv_heads * p.group, p.num_seqs);
-  tree_kernel<KV, kQBf16, D><<<grid, 32, 0, st>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_cap(const CUtensorMap& km, const CUtensorMap& vm, const TreeParams& p, cudaStream_t st) {
+  return p.softcap > 0.f ? launch_t<KV, kQBf16, D, true>(km, vm, p, st) : launch_t<KV, kQBf16, D, false>(km, vm, p, st);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_tree(KvType kv, QType q, int head_dim, const TreeParams& p, cudaStream_t st) {
-  if (kv == KvType::E4M3)
-    return q == QType::BF16 ? launch_tree_t<KvType::E4M3, true, 128>(p, st) : launch_tree_t<KvType::E4M3, false, 128>(p, st);
+bool tree_supported(KvType kv, int head_dim, int group) {
+  return group >= 1 && group <= 16 && (head_dim == 128 || (head_dim == 64 && kv != KvType::E4M3));
+}
+
+bool tree_splits(int64_t max_context_len) { return (max_context_len + kKeys - 1) / kKeys > kWhole; }
+
+int tree_spans(int64_t num_seqs, int num_kv_heads, int group, int max_query_len, int64_t max_context_len) {
+  // (Each factor is capped where more cannot matter, so that no product overflows.)
+  const auto cap = [](int64_t x) { return std::min<int64_t>(x, 1 << 20); };
+  const int64_t items = cap(cap(num_seqs) * num_kv_heads) * cap((static_cast<int64_t>(max_query_len) * group + kRows - 1) / kRows);
+  const int64_t cost = cap(items) * ((max_context_len + kKeys - 1) / kKeys + kItemCost);
+  return static_cast<int>(std::min<int64_t>(kTreeMaxSpans, std::max<int64_t>(1, (cost + kMinSpan - 1) / kMinSpan)));
+}
+
+cudaError_t launch_decode_tree(KvType kv, QType q, int head_dim, const CUtensorMap& km, const CUtensorMap& vm,
+                                  const TreeParams& p, cudaStream_t st) {
   if (kv == KvType::BF16)
-    return head_dim == 128 ? launch_tree_t<KvType::BF16, true, 128>(p, st) : launch_tree_t<KvType::BF16, true, 64>(p, st);
-  return head_dim == 128 ? launch_tree_t<KvType::F16, false, 128>(p, st) : launch_tree_t<KvType::F16, false, 64>(p, st);
+    return head_dim == 128 ? launch_cap<KvType::BF16, true, 128>(km, vm, p, st) : launch_cap<KvType::BF16, true, 64>(km, vm, p, st);
+  if (kv == KvType::F16)
+    return head_dim == 128 ? launch_cap<KvType::F16, false, 128>(km, vm, p, st) : launch_cap<KvType::F16, false, 64>(km, vm, p, st);
+  return q == QType::BF16 ? launch_cap<KvType::E4M3, true, 128>(km, vm, p, st) : launch_cap<KvType::E4M3, false, 128>(km, vm, p, st);
 }
 
 }  // namespace pa
