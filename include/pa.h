@@ -337,8 +337,8 @@ size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int
  * pa_commit_tree -- keep the accepted path of each sequence's drafted tree.
  *   k_cache, v_cache  [num_blocks, Hkv, 16, D] contiguous, any one dtype of F16, BF16 and E4M3; a row
  *                     (D elements) a multiple of 16 bytes.
- *   block_tables, query_start, context_lens  as pa_decode_tree had them (n_s drafted nodes at the end of
- *                     context_lens[s] tokens; query_start's differences alone matter).
+ *   block_tables, query_start, context_lens  as pa_decode_tree had them (n_s <= 256 drafted nodes at the end
+ *                     of context_lens[s] tokens; query_start's differences alone matter).
  *   accepted          [B, P] device I32, last stride 1: the accepted nodes in path order, strictly
  *                     increasing (a parent comes before its children); entries at i >= accepted_lens[s]
  *                     are not read.

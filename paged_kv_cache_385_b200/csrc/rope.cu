@@ -88,9 +88,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_and_cache_kernel(const Rope
   const int v_units = (chunks + 1) / 2;
   const int rotated_heads = p.num_q_heads + p.num_kv_heads;
   const int total = rotated_heads * units + p.num_kv_heads * v_units;
-  const int64_t slot = p.slots[t];
-  const bool store_kv = slot >= 0 && slot < p.num_slots;
-  if ((slot < -1 || slot >= p.num_slots) && threadIdx.x == 0) atomicOr(p.err, 2u);
+  const int64_t slot = p.slots[t];  // not needed before the first store: the rows' loads do not wait for it
 
   struct Unit {
     int c0, c1;  // chunk indices (c1 == chunks: none)
@@ -114,10 +112,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_and_cache_kernel(const Rope
       k = x - u.head * v_units;
       u.kind = 2;
     }
-    if (u.kind != 0 && !store_kv) {
-      u.kind = 3;
-      return;
-    }
     u.mates = u.kind != 2 && k < pair_units;
     if (u.mates) {
       u.c0 = k;
@@ -132,8 +126,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_and_cache_kernel(const Rope
     u.a = load_chunk<VEC>(src + u.c0 * VEC);
     if (u.c1 < chunks) u.b = load_chunk<VEC>(src + u.c1 * VEC);
   };
+  Unit u[kRopeUnits];
+#pragma unroll
+  for (int i = 0; i < kRopeUnits; ++i) load(threadIdx.x + i * kRopeThreads, u[i]);
+  const double pos = static_cast<double>(p.positions[t]);
+  const bool store_kv = slot >= 0 && slot < p.num_slots;
+  if ((slot < -1 || slot >= p.num_slots) && threadIdx.x == 0) atomicOr(p.err, 2u);
   auto finish = [&](const Unit& u) {
-    if (u.kind == 3) return;
+    if (u.kind == 3 || (u.kind != 0 && !store_kv)) return;
     const bool two = u.c1 < chunks;
     float x[VEC], y[VEC];
     const bool turn0 = u.mates || (kPairs && u.kind != 2 && u.c0 * VEC < p.rot);
@@ -193,10 +193,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_and_cache_kernel(const Rope
     }
   };
 
-  Unit u[kRopeUnits];
-#pragma unroll
-  for (int i = 0; i < kRopeUnits; ++i) load(threadIdx.x + i * kRopeThreads, u[i]);
-  const double pos = static_cast<double>(p.positions[t]);
   for (int i = threadIdx.x; i < half; i += kRopeThreads) {
     double turns = pos * static_cast<double>(p.inv_freq[i]) * 0.15915494309189535;  // 1 / (2 pi)
     turns -= rint(turns);

@@ -16,8 +16,9 @@
 // memory, two S buffers in tensor memory), softmax by 4 warps with a row per thread, P over S in tensor
 // memory, O += P V (A from tensor memory). Warps: 0-3 softmax, Q loads and epilogue; 4 TMA producer of K;
 // 5 QK issuer and owner of the tensor memory; 6 TMA producer of V; 7 PV issuer. e4m3 pages land as they
-// are and two more pairs of warps widen them (8-9 K, 10-11 V) into the f16 operand tiles. Two CTAs per SM.
+// are and two more warps widen them (8 K, 9 V) into the f16 operand tiles. Two CTAs per SM.
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "pa_device.cuh"
@@ -46,7 +47,7 @@ struct Layout {
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kQTile = kHalves * kQHalf;
   static constexpr uint32_t kTile = kHalves * kHalf;
-  static constexpr int kKStages = kFp8 ? 2 : (D == 128 ? 3 : 4), kVStages = kFp8 ? 1 : (D == 128 ? 2 : 4);
+  static constexpr int kKStages = kFp8 ? 1 : (D == 128 ? 3 : 4), kVStages = kFp8 || D == 128 ? 2 : 4;
   // e4m3: pages land in rings of their own and are widened into the operand tiles.
   static constexpr uint32_t kRawTile = kFp8 ? kHalf : 0;
   static constexpr int kRawStages = 2;
@@ -57,9 +58,9 @@ struct Layout {
   static constexpr uint32_t kRawVOff = kRawKOff + kRawStages * kRawTile;
   static constexpr uint32_t kBarOff = kRawVOff + kRawStages * kRawTile;
   static constexpr uint32_t kSmemBytes = kBarOff + kBarBytes;
-  static constexpr int kThreads = kFp8 ? 384 : 256;
+  static constexpr int kThreads = kFp8 ? 320 : 256;
   // Scores of a row that its thread holds at a time: all 64 of a block, or, where registers do not
-  // suffice (768 threads an SM, or the cap's arithmetic), 32 that are read twice from tensor memory.
+  // suffice (640 threads an SM, or the cap's arithmetic), 32 that are read twice from tensor memory.
   static constexpr int kHeld = kFp8 || kCap ? 32 : 64;
   // P is 2^(s - m + kShift): f16 keeps 7 more binades of small weights before it rounds them away
   // (2^(8 + 7) is still finite); bf16 has float32's range.
@@ -91,7 +92,7 @@ enum {
   kMeet = 25,    // the softmax warps meet (4)
   kTmemSlot = 26,
   kBadNodes = 27,  // 256 bits: nodes whose V row holds infinities or NaN
-  kRawKFull0 = 31,  // 2 each: e4m3 pages landed, and widened (2 warps)
+  kRawKFull0 = 31,  // 2 each: e4m3 pages landed, and widened
   kRawKEmpty0 = 33,
   kRawVFull0 = 35,
   kRawVEmpty0 = 37,
@@ -195,13 +196,42 @@ __device__ __forceinline__ uint64_t visible_bits(const TreeParams& p, const vola
   return v & low_ones(P->ctx - t0);
 }
 
-// Max (kMax) or min of n values in four independent chains.
-template <bool kMax, int n>
-__device__ __forceinline__ float extreme(const float (&v)[n]) {
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Max of n values (n a multiple of 8), in four independent chains of three-way maxima.
+template <int n>
+__device__ __forceinline__ float largest(const float (&v)[n]) {
   float e[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-  for (int k = 4; k < n; ++k) e[k & 3] = kMax ? fmaxf(e[k & 3], v[k]) : fminf(e[k & 3], v[k]);
-  return kMax ? fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) : fminf(fminf(e[0], e[1]), fminf(e[2], e[3]));
+  for (int k = 4; k + 8 <= n; k += 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = max3(e[i], v[k + 2 * i], v[k + 2 * i + 1]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) e[i] = fmaxf(e[i], v[n - 4 + i]);
+  return fmaxf(max3(e[0], e[1], e[2]), e[3]);
+}
+
+// Two float32 lanes in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -293,19 +323,19 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
   if (threadIdx.x == 0) {
     mbar_init(B(kQFull), 4);
     for (int i = 0; i < L::kKStages; ++i) {
-      mbar_init(B(kKFull0 + i), L::kFp8 ? 2 : 1);
+      mbar_init(B(kKFull0 + i), 1);
       mbar_init(B(kKEmpty0 + i), 1);
     }
     for (int i = 0; i < L::kVStages; ++i) {
-      mbar_init(B(kVFull0 + i), L::kFp8 ? 2 : 1);
+      mbar_init(B(kVFull0 + i), 1);
       mbar_init(B(kVEmpty0 + i), 1);
     }
     if constexpr (L::kFp8) {
       for (int i = 0; i < L::kRawStages; ++i) {
         mbar_init(B(kRawKFull0 + i), 1);
-        mbar_init(B(kRawKEmpty0 + i), 2);
+        mbar_init(B(kRawKEmpty0 + i), 1);
         mbar_init(B(kRawVFull0 + i), 1);
-        mbar_init(B(kRawVEmpty0 + i), 2);
+        mbar_init(B(kRawVEmpty0 + i), 1);
       }
     }
     for (int i = 0; i < 2; ++i) {
@@ -315,7 +345,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     }
     for (int i = 0; i < kParts; ++i) {
       mbar_init(B(kPartFull0 + i), 1);
-      mbar_init(B(kPartEmpty0 + i), L::kFp8 ? 11 : 7);  // V producer, issuers, 4 softmax warps, 4 widening ones
+      mbar_init(B(kPartEmpty0 + i), L::kFp8 ? 9 : 7);  // V producer, issuers, 4 softmax warps, 2 widening ones
     }
     mbar_init(B(kOFree), 4);
     mbar_init(B(kMeet), 4);
@@ -378,9 +408,12 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     return true;
   };
 
-  // e4m3: two warps widen one ring's pages into its operand tiles, exactly (every code is an f16).
+  // e4m3: a warp widens one ring's pages into its operand tiles, exactly (every code is an f16).
   auto widen_all = [&](uint32_t raw_off, int raw_full0, int raw_empty0, uint32_t off, int ns, int full0, int empty0) {
-    const int t = threadIdx.x & 63;
+    // 16 codes at a time: chunk c of a row becomes chunks 2c and 2c + 1 of the widened one. Of eight
+    // lanes, four read a row's first half and four its neighbour's second half, so that neither their
+    // loads nor their stores meet on a bank.
+    const int c = lane & 7, dst0 = (c >> 2) * kHalf, e = 2 * c & 7;
     for (int it = 0, g = 0;; ++it) {
       const uint64_t deadline = globaltimer_ns() + kWaitNs;
       const volatile Part* P = take_part(it, deadline);
@@ -393,31 +426,26 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
       for (int j = 0; j < blocks; ++j, ++g) {
         const int rs = g % L::kRawStages, st = g % ns;
         const bool got = mbar_wait_bounded(B(raw_full0 + rs), (g / L::kRawStages) & 1, deadline) &&
-                         (g < ns || mbar_wait_bounded(B(empty0 + st), ((g / ns) - 1) & 1, deadline));
+                         (g < ns || mbar_wait_bounded_poll(B(empty0 + st), ((g / ns) - 1) & 1, deadline));
         if (!__all_sync(kFull, got)) {
           ok = false;
           break;
         }
-        const uint32_t raw = base + raw_off + rs * kHalf, dst = base + off + st * L::kTile;
+        const uint32_t raw = base + raw_off + rs * kHalf, dst = base + off + st * L::kTile + dst0;
 #pragma unroll 4
-        for (int i = 0; i < 8; ++i) {
-          const int row = (t >> 3) + 8 * i, c = t & 7;  // 16 codes; 8 lanes read a row's 128 bytes
+        for (int i = 0; i < kKeys / 4; ++i) {
+          const int row = ((lane >> 3) + 4 * i) ^ (c >> 2);
           uint32_t w[4], o[8];
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                        : "r"(raw + row * 128 + ((c ^ (row & 7)) << 4)));
 #pragma unroll
           for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2x2(w[k], o[2 * k], o[2 * k + 1]);
-          // Chunks 2c and 2c + 1 of the widened row. Lanes of the second half take the odd one first, so
-          // that the eight lanes of a row never meet on a bank.
-          const uint32_t line = dst + (c >> 2) * kHalf + row * 128;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int odd = h ^ (c >> 2), e = (2 * c + odd) & 7;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + ((e ^ (row & 7)) << 4)),
-                         "r"(odd ? o[4] : o[0]), "r"(odd ? o[5] : o[1]), "r"(odd ? o[6] : o[2]), "r"(odd ? o[7] : o[3])
+          for (int h = 0; h < 2; ++h)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + row * 128 + (((e + h) ^ (row & 7)) << 4)),
+                         "r"(o[4 * h]), "r"(o[4 * h + 1]), "r"(o[4 * h + 2]), "r"(o[4 * h + 3])
                          : "memory");
-          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -433,7 +461,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
 
   if (warp >= 8) {
     if constexpr (L::kFp8) {
-      if (warp < 10) widen_all(L::kRawKOff, kRawKFull0, kRawKEmpty0, L::kKOff, L::kKStages, kKFull0, kKEmpty0);
+      if (warp == 8) widen_all(L::kRawKOff, kRawKFull0, kRawKEmpty0, L::kKOff, L::kKStages, kKFull0, kKEmpty0);
       else widen_all(L::kRawVOff, kRawVFull0, kRawVEmpty0, L::kVOff, L::kVStages, kVFull0, kVEmpty0);
     }
   } else if (warp == 4) {
@@ -492,8 +520,8 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
           // Buffer g & 1 holds P(g - 2) until P(g - 2).V has run. O_done is two barriers by parity: the
           // one waited for here next completes for P(g).V, which needs the S issued below.
           const int st = g % L::kKStages;
-          if ((g >= 2 && !mbar_wait_bounded(B(kODone0 + (g & 1)), ((g - 2) >> 1) & 1, deadline)) ||
-              !mbar_wait_bounded(B(kKFull0 + st), (g / L::kKStages) & 1, deadline)) {
+          if ((g >= 2 && !mbar_wait_bounded_poll(B(kODone0 + (g & 1)), ((g - 2) >> 1) & 1, deadline)) ||
+              !mbar_wait_bounded_poll(B(kKFull0 + st), (g / L::kKStages) & 1, deadline)) {
             ok = false;
             break;
           }
@@ -527,8 +555,8 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         if (it > 0) ok = mbar_wait_bounded(B(kOFree), (it - 1) & 1, deadline);
         for (int j = 0; j < blocks && ok; ++j, ++g) {
           const int st = g % L::kVStages;
-          if (!mbar_wait_bounded(B(kPFull0 + (g & 1)), (g >> 1) & 1, deadline) ||
-              !mbar_wait_bounded(B(kVFull0 + st), (g / L::kVStages) & 1, deadline)) {
+          if (!mbar_wait_bounded_poll(B(kPFull0 + (g & 1)), (g >> 1) & 1, deadline) ||
+              !mbar_wait_bounded_poll(B(kVFull0 + st), (g / L::kVStages) & 1, deadline)) {
             ok = false;
             break;
           }
@@ -549,7 +577,6 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     }
   } else {
     // ---- softmax warps: thread = row -----------------------------------------------------------------
-    const int r = threadIdx.x;  // 0..127, the row's TMEM lane
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     const int G = p.group;
     const uint32_t inv_g = (65536u + G - 1) / G;
@@ -560,16 +587,26 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     const float cap2 = kCap ? p.softcap * 1.4426950408889634f : 0.f;
     const float cap_u = kCap ? 2.f * sl2 / p.softcap : 0.f;
     volatile uint32_t* bad_nodes = reinterpret_cast<volatile uint32_t*>(smem + L::kBarOff + 8 * kBadNodes);
-    int meets = 0;
-    if (r == 0 && p.ws_desc) p.ws_desc[blockIdx.x * kTreeDescInts + 4] = 0;
+    int meets = 0, turn = 0;
+    if (threadIdx.x == 0 && p.ws_desc) p.ws_desc[blockIdx.x * kTreeDescInts + 4] = 0;
 
     auto score = [&](float s) -> float {  // a raw product in log2 units
       if constexpr (kCap) return fmaf(-2.f * cap2, rcp_approx(1.f + ex2(s * cap_u)), cap2);
       else return s * sl2;
     };
-    auto weight = [&](float s, float nref) -> float {
-      if constexpr (kCap) return ex2(score(s) + nref);
-      else return ex2(fmaf(s, sl2, nref));
+    // Two weights 2^(score - reference): x is replaced by them.
+    auto weights = [&](float& x0, float& x1, float nref) {
+      float2 t;
+      if constexpr (kCap) {
+        t = fma2(make_float2(x0, x1), make_float2(cap_u, cap_u), make_float2(0.f, 0.f));
+        t = add2(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
+        t = fma2(make_float2(rcp_approx(t.x), rcp_approx(t.y)), make_float2(-2.f * cap2, -2.f * cap2),
+                 make_float2(cap2 + nref, cap2 + nref));
+      } else {
+        t = fma2(make_float2(x0, x1), make_float2(sl2, sl2), make_float2(nref, nref));
+      }
+      x0 = ex2(t.x);
+      x1 = ex2(t.y);
     };
     // The four warps meet (a bounded wait: a warp that gave up does not come).
     auto meet = [&](uint64_t deadline) -> bool {
@@ -579,27 +616,29 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
       ++meets;
       return __all_sync(kFull, got);
     };
+    // Few rows keep only some warps busy. Those of the second half of the CTAs, which share their SMs with
+    // the first half's, are turned by half a tile, so that the two use different quarters of the SM.
+    auto turn_of = [&](int rows_left) { return rows_left <= kRows / 2 && blockIdx.x * 2 >= gridDim.x ? kRows / 2 : 0; };
     // A part's Q rows into the swizzled tile, as asynchronous copies of 16-byte chunks, a row's by
-    // neighbouring lanes; rows past the last are zero. start_q may run once the QKs of the part before
-    // have (this warp has seen its last S), finish_q hands the tile to the QK issuer.
+    // neighbouring lanes; rows past the last keep what the tile held (each row's products are its own).
+    // start_q may run once the QKs of the part before have (this warp has seen its last S), finish_q
+    // hands the tile to the QK issuer.
     constexpr int kRowChunks = D / 8;
     auto q_addr = [&](int x) -> uint32_t {
       const int row = warp * 32 + x / kRowChunks, c = x % kRowChunks;
       return base + L::kQOff + (c >> 3) * kQHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4);
     };
     auto start_q = [&](const volatile Part* P) {
-      const int row0 = P->tile * kRows + warp * 32, rows = P->rows, head0 = P->hk * G;
-      const uint16_t* q0 = static_cast<const uint16_t*>(p.q) + P->q0 * p.q_stride_t;
+      const int row0 = P->tile * kRows, left = min(P->rows - row0, kRows), head0 = P->hk * G, c = lane % kRowChunks;
+      const int from = (warp * 32 - turn_of(left)) & (kRows - 1);  // the warp's first row of the tile
+      const uint16_t* q0 = static_cast<const uint16_t*>(p.q) + P->q0 * p.q_stride_t + c * 8;
 #pragma unroll 4
       for (int x = lane; x < 32 * kRowChunks; x += 32) {
-        const int R = row0 + x / kRowChunks, node = div_group(R, inv_g);
-        const uint16_t* src = q0;
-        uint32_t bytes = 0;
-        if (R < rows) {
-          src = q0 + node * p.q_stride_t + (head0 + R - node * G) * p.q_stride_h + x % kRowChunks * 8;
-          bytes = 16;
-        }
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_addr(x)), "l"(src), "r"(bytes) : "memory");
+        const int row = from + x / kRowChunks;
+        if (row >= left) break;
+        const int R = row0 + row, node = div_group(R, inv_g);
+        const uint16_t* src = q0 + node * p.q_stride_t + (head0 + R - node * G) * p.q_stride_h;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(q_addr(x)), "l"(src) : "memory");
       }
     };
     auto finish_q = [&] {
@@ -637,112 +676,137 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         start_q(P);
         finish_q();
       }
-      const int rows_left = P->rows - P->tile * kRows;
+      // The tile's rows lie on the tensor-memory lanes in order, from lane `turn` on.
+      const int rows_left = min(P->rows - P->tile * kRows, kRows);
+      turn = turn_of(rows_left);
+      const int r = (static_cast<int>(threadIdx.x) - turn) & (kRows - 1);
       const bool valid = r < rows_left;
-      const bool working = warp * 32 < rows_left;  // warps past the last row only keep step
+      const bool working = ((warp * 32 - turn) & (kRows - 1)) < rows_left;  // warps without a row only keep step
       const int node = valid ? div_group(P->tile * kRows + r, inv_g) : 0;
       const int j_mask = P->start / kKeys;  // the first block that holds a drafted node or the end
       const bool had_tail = j1 > j_mask;
       if (had_tail) {  // no warp reads the bits of the part before any more; they are cleared
         ok = meet(deadline);
-        if (r < 8) bad_nodes[r] = 0u;
+        if (threadIdx.x < 8) bad_nodes[threadIdx.x] = 0u;
         ok = ok && meet(deadline);
         if (!ok) break;
+        if (p.mask && valid) {
+          const uint64_t* words = p.mask + static_cast<int64_t>(P->q0 + node) * p.mask_words;
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(words));
+        }
       }
-      float m = -INFINITY, l = 0.f;
-      for (int j = j0; j < j1; ++j) {
+      float m = -INFINITY, l = 0.f;  // m: the reference P and l are taken against (lazily raised)
+      // Block j's P from its S. kMasked: some row may not see all of its keys.
+      auto softmax = [&](auto masked_tag, int j) -> bool {
+        constexpr bool kMasked = decltype(masked_tag)::value;
         const int gb = g + j - j0;
-        const bool got = mbar_wait_bounded(B(kSFull0 + (gb & 1)), (gb >> 1) & 1, deadline);
-        if (!__all_sync(kFull, got)) {
+        const uint32_t tS = tS0 + (gb & 1) * kKeys + lane_off;
+        uint64_t vis = ~0ull;
+        if constexpr (kMasked) {
+          vis = valid ? visible_bits(p, P, node, j * kKeys) : 0ull;
+          __syncwarp();
+        }
+        // The block's largest score in log2 units: cap and scale are monotone, so they are applied to the
+        // largest raw score alone.
+        float sv[L::kHeld], top = -INFINITY;
+        if constexpr (L::kHeld == kKeys) tc05::ld64(tS, sv);
+#pragma unroll
+        for (int h = 0; h < kKeys / L::kHeld; ++h) {
+          if constexpr (L::kHeld == 32) tc05::ld32(tS + 32 * h, sv);
+          if constexpr (kMasked) {
+            const uint64_t bits = vis >> (32 * h);
+#pragma unroll
+            for (int k = 0; k < L::kHeld; ++k)
+              if (!(static_cast<uint32_t>(bits >> (k & 32)) >> (k & 31) & 1u)) sv[k] = -INFINITY;
+          }
+          top = fmaxf(top, largest(sv));
+        }
+        const float mx = kMasked && vis == 0ull ? -INFINITY : score(top);
+        // (Each row raises its own reference, so that its result does not depend on its neighbours'.)
+        const bool mine = mx > m + kLazyRescale;
+        const bool raise = __any_sync(kFull, mine);
+        float alpha = 1.f;
+        if (mine) {
+          alpha = m == -INFINITY ? 0.f : ex2(m - mx);
+          m = mx;
+        }
+        const float nref = L::kShift - (m == -INFINITY ? 0.f : m);
+        float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int h = 0; h < kKeys / 32; ++h) {
+          // (P of the first half lies over that half's scores: the second's are still there.)
+          if constexpr (L::kHeld == 32) tc05::ld32(tS + 32 * h, sv);
+          float* x = sv + (L::kHeld == 32 ? 0 : 32 * h);
+          const uint32_t bits = static_cast<uint32_t>(vis >> (32 * h));
+          uint32_t wd[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            weights(x[2 * k], x[2 * k + 1], nref);
+            if constexpr (kMasked) {
+              if (!(bits >> (2 * k) & 1u)) x[2 * k] = 0.f;
+              if (!(bits >> (2 * k + 1) & 1u)) x[2 * k + 1] = 0.f;
+            }
+            rs[k & 3] = add2(rs[k & 3], make_float2(x[2 * k], x[2 * k + 1]));
+            wd[k] = pack2<kBf16>(x[2 * k], x[2 * k + 1]);
+          }
+          tc05::st16u_nowait(tS + 16 * h, wd);
+        }
+        const float2 sum = add2(add2(rs[0], rs[1]), add2(rs[2], rs[3]));
+        l = l * alpha + (sum.x + sum.y);
+        // O's rescale waits for the P.V before it. Its barrier next completes for P(gb + 1).V, which
+        // needs this warp's P(gb + 1): never two phases ahead.
+        if (raise && j > j0) {
+          const bool done = mbar_wait_bounded(B(kODone0 + ((gb - 1) & 1)), ((gb - 1) >> 1) & 1, deadline);
+          if (!__all_sync(kFull, done)) return false;
+          tc05::fence_after_sync();
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float v[32];
+            tc05::ld32(tO + lane_off + c * 32, v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] *= alpha;
+            tc05::st32(tO + lane_off + c * 32, v);
+          }
+        }
+        tc05::st_wait();
+        return true;
+      };
+      auto got_s = [&](int gb) -> bool {
+        const bool got = mbar_wait_bounded_poll(B(kSFull0 + (gb & 1)), (gb >> 1) & 1, deadline);
+        if (!__all_sync(kFull, got)) return false;
+        tc05::fence_after_sync();
+        return true;
+      };
+      auto give_p = [&](int gb) {
+        tc05::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(B(kPFull0 + (gb & 1)));
+      };
+      // The blocks that every row sees whole, but for the part's last: a short loop.
+      int j = j0;
+      for (const int whole_end = min(j_mask, j1 - 1); j < whole_end; ++j) {
+        const int gb = g + j - j0;
+        ok = got_s(gb);
+        if (!ok || (working && !softmax(std::false_type{}, j))) {
           ok = false;
           break;
         }
-        tc05::fence_after_sync();
-        const int t0 = j * kKeys;
-        // The next part's Q starts on its way as soon as this part's last QK has run.
-        if (j == j1 - 1) {
+        give_p(gb);
+      }
+#pragma unroll 1
+      for (; ok && j < j1; ++j) {
+        const int gb = g + j - j0;
+        ok = got_s(gb);
+        if (!ok) break;
+        if (j == j1 - 1) {  // the part's last QK has run: the next part's Q starts on its way
           const volatile Part* N = take_part(it + 1, deadline);
           ok = __all_sync(kFull, N != nullptr);
           if (!ok) break;
           if (N->j0 < N->j1) start_q(N);
         }
-        if (working) {
-          const uint32_t tS = tS0 + (gb & 1) * kKeys + lane_off;
-          const bool masked = j >= j_mask;
-          uint64_t vis = ~0ull;
-          if (masked) {
-            vis = valid ? visible_bits(p, P, node, t0) : 0ull;
-            __syncwarp();
-          }
-          // The block's largest score in log2 units: cap and scale are monotone, so they are applied to the
-          // largest raw score alone.
-          float sv[L::kHeld], top = -INFINITY;
-          if constexpr (L::kHeld == kKeys) tc05::ld64(tS, sv);
-#pragma unroll
-          for (int h = 0; h < kKeys / L::kHeld; ++h) {
-            if constexpr (L::kHeld == 32) tc05::ld32(tS + 32 * h, sv);
-            if (masked) {
-              const uint64_t bits = vis >> (32 * h);
-#pragma unroll
-              for (int k = 0; k < L::kHeld; ++k)
-                if (!(static_cast<uint32_t>(bits >> (k & 32)) >> (k & 31) & 1u)) sv[k] = -INFINITY;
-            }
-            top = fmaxf(top, extreme<true, L::kHeld>(sv));
-          }
-          const float mx = vis == 0ull ? -INFINITY : score(top);
-          const bool raise = __any_sync(kFull, mx > m + kLazyRescale);
-          float alpha = 1.f;
-          if (raise) {
-            const float mn = fmaxf(m, mx);
-            alpha = m == -INFINITY ? (mn == -INFINITY ? 1.f : 0.f) : ex2(m - mn);
-            m = mn;
-          }
-          const float nref = L::kShift - (m == -INFINITY ? 0.f : m);
-          float rs[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int h = 0; h < kKeys / 32; ++h) {
-            // (P of the first half lies over that half's scores: the second's are still there.)
-            if constexpr (L::kHeld == 32) tc05::ld32(tS + 32 * h, sv);
-            float* x = sv + (L::kHeld == 32 ? 0 : 32 * h);
-            uint32_t wd[16];
-            if (!masked) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                x[k] = weight(x[k], nref);
-                rs[k & 3] += x[k];
-              }
-            } else {
-              const uint32_t bits = static_cast<uint32_t>(vis >> (32 * h));
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                x[k] = bits >> k & 1u ? weight(x[k], nref) : 0.f;
-                rs[k & 3] += x[k];
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < 16; ++k) wd[k] = pack2<kBf16>(x[2 * k], x[2 * k + 1]);
-            tc05::st16u_nowait(tS + 16 * h, wd);
-          }
-          l = l * alpha + ((rs[0] + rs[1]) + (rs[2] + rs[3]));
-          // O's rescale waits for the P.V before it. Its barrier next completes for P(gb + 1).V, which
-          // needs this warp's P(gb + 1): never two phases ahead.
-          if (raise && j > j0) {
-            const bool done = mbar_wait_bounded(B(kODone0 + ((gb - 1) & 1)), ((gb - 1) >> 1) & 1, deadline);
-            if (!__all_sync(kFull, done)) {
-              ok = false;
-              break;
-            }
-            tc05::fence_after_sync();
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              float v[32];
-              tc05::ld32(tO + lane_off + c * 32, v);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] *= alpha;
-              tc05::st32(tO + lane_off + c * 32, v);
-            }
-          }
-          tc05::st_wait();
+        if (working && !softmax(std::true_type{}, j)) {
+          ok = false;
+          break;
         }
         // V rows of drafted nodes and behind the context. A weight of 0 must take nothing from a row that
         // holds infinities or NaN: rows behind the context are zeroed, and a node's non-finite elements
@@ -756,8 +820,9 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
           constexpr int C = D / 8;
           constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u;
           const uint32_t vb = base + L::kVOff + (gb % L::kVStages) * L::kTile;
-          const int start = P->start, first = max(start - t0, 0), held = P->ctx - t0;
-          for (int x = r; x < (kKeys - first) * C; x += 128) {
+          const int t0 = j * kKeys, start = P->start, first = max(start - t0, 0), held = P->ctx - t0;
+#pragma unroll 2
+          for (int x = threadIdx.x; x < (kKeys - first) * C; x += 128) {
             const int row = first + x / C, c = x % C;
             const uint32_t a = vb + (c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4);
             uint32_t w[4], odd = 0u;
@@ -779,9 +844,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        tc05::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(B(kPFull0 + (gb & 1)));
+        give_p(gb);
       }
       if (!ok) break;
       const int gl = g + j1 - j0 - 1;
@@ -815,7 +878,9 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
           tc05::ld32(tO + lane_off + c * 32, v);
           if (any_bad && valid) {  // non-finite values of nodes that this row sees
             const int32_t* bt = p.block_tables + static_cast<int64_t>(P->s) * p.bt_stride;
+#pragma unroll 1
             for (int w = 0; w < 8; ++w) {
+#pragma unroll 1
               for (uint32_t bits = bad_nodes[w]; bits; bits &= bits - 1) {
                 const int nd = 32 * w + __ffs(bits) - 1, t = P->start + nd;
                 if (!(visible_bits(p, P, node, t) & 1ull)) continue;
@@ -854,7 +919,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         }
         if (valid && !whole) p.ws_ml[slot * kRows + r] = make_float2(m, l);
       }
-      if (r == 0 && !whole && first == static_cast<int>(blockIdx.x)) {
+      if (threadIdx.x == 0 && !whole && first == static_cast<int>(blockIdx.x)) {
         int32_t* d = p.ws_desc + blockIdx.x * kTreeDescInts;
         d[0] = P->q0;
         d[1] = P->tile;

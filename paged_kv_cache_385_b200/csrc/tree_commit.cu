@@ -6,31 +6,58 @@
 // groups, each read in full before any of it is written, so the in-place move needs no copy (and a
 // later group reads nothing that an earlier one wrote).
 //
-// A few rows of a few hundred bytes: latency bounds it. One CTA per (sequence, KV head, cache), so
-// that all of a call's rows are in flight at once; each thread carries 16-byte chunks of the rows.
+// A few rows of a few hundred bytes per head: latency bounds it. A CTA takes a sequence and some of its
+// 2 Hkv (KV head, cache) pools; it looks the path's rows up in the block table once, into shared memory,
+// and its threads then carry 16-byte chunks, kCommitChunks of them in flight. The pools are spread over
+// as many CTAs as fill the GPU: few sequences, few chunks to a thread.
+#include <algorithm>
+
 #include "internal.h"
 #include "pa_device.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kCommitThreads = 128;
-constexpr int kCommitChunks = 4;  // 16-byte chunks a thread holds between reading and writing
+constexpr int kCommitThreads = 256;
+constexpr int kCommitChunks = 8;  // 16-byte chunks a thread holds between reading and writing
+constexpr int kCommitCtas = 4 * 148;
 
 __global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(const CommitParams p) {
+  // Rows of KV head 0 that move, as (block * Hkv * 16 + offset): from, to; -1 where the table names no
+  // block of the pool.
+  __shared__ int64_t from[kTreeMaxNodes], to[kTreeMaxNodes];
   const int s = blockIdx.x;
-  const int hk = blockIdx.y >> 1;
   const int ctx = p.context_lens[s];
-  const int n = p.query_start[s + 1] - p.query_start[s];
+  const int64_t n64 = static_cast<int64_t>(p.query_start[s + 1]) - p.query_start[s];
   const int taken = p.accepted_lens[s];
   const int32_t* path = p.accepted + static_cast<int64_t>(s) * p.accepted_stride;
-  const bool in_range = n >= 0 && n <= ctx && ctx <= p.max_blocks * 16;
+  const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.bt_stride;
+  const bool in_range = n64 >= 0 && n64 <= min(ctx, kTreeMaxNodes) && ctx <= p.max_blocks * 16;
+  const int n = in_range ? static_cast<int>(n64) : 0;
   bool good = in_range && taken >= 0 && taken <= min(p.path_len, n);
+  const int start = ctx - n;
+  int kept = 0;  // a path's leading nodes 0, 1, 2, ... are in place already
   if (good) {
-    bool mine = true;
-    for (int i = threadIdx.x; i < taken; i += kCommitThreads)
-      mine = mine && path[i] < n && path[i] > (i ? path[i - 1] : -1);
+    const int i = threadIdx.x;
+    bool mine = true, stays = false;
+    if (i < taken) {
+      const int node = path[i];
+      mine = node < n && node > (i ? path[i - 1] : -1);
+      stays = mine && node == i;
+      if (mine && !stays) {
+        auto row = [&](int at) -> int64_t {
+          const int b = table[at >> 4];
+          if (b >= 0 && b < p.num_blocks) return static_cast<int64_t>(b) * p.num_kv_heads * 16 + (at & 15);
+          atomicOr(p.err, 1u);
+          return -1;
+        };
+        from[i] = row(start + node);
+        to[i] = row(start + i);
+      }
+    }
+    static_assert(kCommitThreads >= kTreeMaxNodes, "a thread per path node");
     good = __syncthreads_and(mine);
+    kept = __syncthreads_count(stays);
   }
   if (blockIdx.y == 0 && threadIdx.x == 0) {
     if (p.new_context_lens) p.new_context_lens[s] = good ? ctx - n + taken : ctx;
@@ -38,47 +65,41 @@ __global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(const Commi
   }
   if (!good) return;
 
-  uint8_t* pool = static_cast<uint8_t*>(blockIdx.y & 1 ? p.v_cache : p.k_cache);
-  const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.bt_stride;
-  const int start = ctx - n, chunks = p.row_bytes / 16;
-  auto row = [&](int node) -> uint4* {  // the node's row, or null where the table names no block of the pool
-    const int at = start + node, b = table[at >> 4];
-    if (b < 0 || b >= p.num_blocks) {
-      atomicOr(p.err, 1u);
-      return nullptr;
-    }
-    return reinterpret_cast<uint4*>(pool + ((static_cast<int64_t>(b) * p.num_kv_heads + hk) * 16 + (at & 15)) * p.row_bytes);
-  };
-  const int64_t total = static_cast<int64_t>(taken) * chunks;
+  // Chunk x of this CTA: (pool, path node, 16 bytes of the row), path nodes ascending within a pool.
+  const int pools = 2 * p.num_kv_heads, chunks = p.row_bytes / 16, per_pool = (taken - kept) * chunks;
+  const int pool0 = static_cast<int>(static_cast<int64_t>(pools) * blockIdx.y / gridDim.y);
+  const int pool1 = static_cast<int>(static_cast<int64_t>(pools) * (blockIdx.y + 1) / gridDim.y);
+  const int64_t total = static_cast<int64_t>(pool1 - pool0) * per_pool;
   for (int64_t base = 0; base < total; base += kCommitThreads * kCommitChunks) {
     uint4 v[kCommitChunks];
-    uint4* to[kCommitChunks];
+    uint4* dst[kCommitChunks];
 #pragma unroll
     for (int k = 0; k < kCommitChunks; ++k) {
       const int64_t x = base + k * kCommitThreads + threadIdx.x;
-      to[k] = nullptr;
+      dst[k] = nullptr;
       if (x >= total) continue;
-      const int i = static_cast<int>(x / chunks), c = static_cast<int>(x - static_cast<int64_t>(i) * chunks);
-      const int node = path[i];
-      if (node == i) continue;
-      const uint4* from = row(node);
-      uint4* dst = row(i);
-      if (!from || !dst) continue;
-      v[k] = from[c];
-      to[k] = dst + c;
+      const int pool = static_cast<int>(x / per_pool), y = static_cast<int>(x - static_cast<int64_t>(pool) * per_pool);
+      const int i = kept + y / chunks, c = y % chunks;
+      const int hk = (pool0 + pool) >> 1;
+      uint8_t* rows = static_cast<uint8_t*>((pool0 + pool) & 1 ? p.v_cache : p.k_cache);
+      const int64_t a = from[i], b = to[i];
+      if (a < 0 || b < 0) continue;
+      v[k] = *reinterpret_cast<const uint4*>(rows + (a + hk * 16) * p.row_bytes + c * 16);
+      dst[k] = reinterpret_cast<uint4*>(rows + (b + hk * 16) * p.row_bytes + c * 16);
     }
     __syncthreads();  // the group's rows are read before any of it is written
 #pragma unroll
     for (int k = 0; k < kCommitChunks; ++k)
-      if (to[k]) *to[k] = v[k];
+      if (dst[k]) *dst[k] = v[k];
   }
 }
 
 }  // namespace
 
 cudaError_t launch_commit_tree(const CommitParams& p, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(p.num_seqs), static_cast<unsigned>(2 * p.num_kv_heads));
-  commit_tree_kernel<<<grid, kCommitThreads, 0, st>>>(p);
+  const int pools = 2 * p.num_kv_heads;
+  const int per_seq = std::min(pools, std::max(1, (kCommitCtas + p.num_seqs - 1) / p.num_seqs));
+  commit_tree_kernel<<<dim3(static_cast<unsigned>(p.num_seqs), static_cast<unsigned>(per_seq)), kCommitThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
