@@ -16,7 +16,8 @@
 // memory, two S buffers in tensor memory), softmax by 4 warps with a row per thread, P over S in tensor
 // memory, O += P V (A from tensor memory). Warps: 0-3 softmax, Q loads and epilogue; 4 TMA producer of K;
 // 5 QK issuer and owner of the tensor memory; 6 TMA producer of V; 7 PV issuer. e4m3 pages land as they
-// are and two more warps widen them (8 K, 9 V) into the f16 operand tiles. Two CTAs per SM.
+// are (warp 4 brings both) and two pairs of warps widen them into the f16 operand tiles (8-9 K, 6 and 10 V).
+// Two CTAs per SM.
 #include <algorithm>
 #include <type_traits>
 
@@ -47,10 +48,10 @@ struct Layout {
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kQTile = kHalves * kQHalf;
   static constexpr uint32_t kTile = kHalves * kHalf;
-  static constexpr int kKStages = kFp8 ? 1 : (D == 128 ? 3 : 4), kVStages = kFp8 || D == 128 ? 2 : 4;
+  static constexpr int kKStages = kFp8 ? 1 : (D == 128 ? 3 : 4), kVStages = kFp8 ? 1 : (D == 128 ? 2 : 4);
   // e4m3: pages land in rings of their own and are widened into the operand tiles.
   static constexpr uint32_t kRawTile = kFp8 ? kHalf : 0;
-  static constexpr int kRawStages = 2;
+  static constexpr int kRawStages = 3;
   static constexpr uint32_t kQOff = 0;
   static constexpr uint32_t kKOff = kQTile;
   static constexpr uint32_t kVOff = kKOff + kKStages * kTile;
@@ -58,9 +59,9 @@ struct Layout {
   static constexpr uint32_t kRawVOff = kRawKOff + kRawStages * kRawTile;
   static constexpr uint32_t kBarOff = kRawVOff + kRawStages * kRawTile;
   static constexpr uint32_t kSmemBytes = kBarOff + kBarBytes;
-  static constexpr int kThreads = kFp8 ? 320 : 256;
+  static constexpr int kThreads = kFp8 ? 352 : 256;
   // Scores of a row that its thread holds at a time: all 64 of a block, or, where registers do not
-  // suffice (640 threads an SM, or the cap's arithmetic), 32 that are read twice from tensor memory.
+  // suffice (704 threads an SM, or the cap's arithmetic), 32 that are read twice from tensor memory.
   static constexpr int kHeld = kFp8 || kCap ? 32 : 64;
   // P is 2^(s - m + kShift): f16 keeps 7 more binades of small weights before it rounds them away
   // (2^(8 + 7) is still finite); bf16 has float32's range.
@@ -92,13 +93,13 @@ enum {
   kMeet = 25,    // the softmax warps meet (4)
   kTmemSlot = 26,
   kBadNodes = 27,  // 256 bits: nodes whose V row holds infinities or NaN
-  kRawKFull0 = 31,  // 2 each: e4m3 pages landed, and widened
-  kRawKEmpty0 = 33,
-  kRawVFull0 = 35,
-  kRawVEmpty0 = 37,
-  kPartFull0 = 39,   // kParts: a part is written (the K producer)
-  kPartEmpty0 = 43,  // kParts: every role has left it
-  kPart0 = 48,       // kParts parts
+  kRawKFull0 = 31,  // 3 each: e4m3 pages landed, and widened (2 warps)
+  kRawKEmpty0 = 34,
+  kRawVFull0 = 37,
+  kRawVEmpty0 = 40,
+  kPartFull0 = 43,   // kParts: a part is written (the K producer)
+  kPartEmpty0 = 47,  // kParts: every role has left it
+  kPart0 = 52,       // kParts parts
 };
 static_assert(kPartFull0 + kParts <= kPartEmpty0 && kPartEmpty0 + kParts <= kPart0, "barrier slots");
 static_assert(sizeof(Part) == 48 && 8 * kPart0 % 16 == 0 && 8 * kPart0 + kParts * sizeof(Part) <= kBarBytes, "barrier area");
@@ -323,19 +324,19 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
   if (threadIdx.x == 0) {
     mbar_init(B(kQFull), 4);
     for (int i = 0; i < L::kKStages; ++i) {
-      mbar_init(B(kKFull0 + i), 1);
+      mbar_init(B(kKFull0 + i), L::kFp8 ? 2 : 1);
       mbar_init(B(kKEmpty0 + i), 1);
     }
     for (int i = 0; i < L::kVStages; ++i) {
-      mbar_init(B(kVFull0 + i), 1);
+      mbar_init(B(kVFull0 + i), L::kFp8 ? 2 : 1);
       mbar_init(B(kVEmpty0 + i), 1);
     }
     if constexpr (L::kFp8) {
       for (int i = 0; i < L::kRawStages; ++i) {
         mbar_init(B(kRawKFull0 + i), 1);
-        mbar_init(B(kRawKEmpty0 + i), 1);
+        mbar_init(B(kRawKEmpty0 + i), 2);
         mbar_init(B(kRawVFull0 + i), 1);
-        mbar_init(B(kRawVEmpty0 + i), 1);
+        mbar_init(B(kRawVEmpty0 + i), 2);
       }
     }
     for (int i = 0; i < 2; ++i) {
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     }
     for (int i = 0; i < kParts; ++i) {
       mbar_init(B(kPartFull0 + i), 1);
-      mbar_init(B(kPartEmpty0 + i), L::kFp8 ? 9 : 7);  // V producer, issuers, 4 softmax warps, 2 widening ones
+      mbar_init(B(kPartEmpty0 + i), L::kFp8 ? 10 : 7);  // issuers, 4 softmax warps; V producer or 4 widening warps
     }
     mbar_init(B(kOFree), 4);
     mbar_init(B(kMeet), 4);
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kBarOff + 8 * kTmemSlot);
   const uint32_t tS0 = tmem, tO = tmem + 2 * kKeys;
   bool ok = true;
-  int issued = 0;  // producer lanes: fills issued (for the drain after a failure)
+  int issued_k = 0, issued_v = 0;  // producer lanes: fills issued (for the drain after a failure)
   constexpr uint64_t kWaitNs = 2000000000ull;
 
   // The K producer walks the span and hands on its parts; every role takes the same parts and blocks. g
@@ -371,17 +372,29 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     return parts + it % kParts;
   };
   auto leave_part = [&](int it) { mbar_arrive(B(kPartEmpty0 + it % kParts)); };
-  // The part's pages of blocks j0 .. j1 - 1 into a ring of ns stages.
-  auto produce = [&](const volatile Part* P, int g, const CUtensorMap* map, uint32_t off, int ns, int full0, int empty0,
-                     uint64_t deadline) -> bool {
+  // The part's pages of blocks j0 .. j1 - 1 into K's ring, V's, or (e4m3) both.
+  constexpr int kRingK = L::kFp8 ? L::kRawStages : L::kKStages, kRingV = L::kFp8 ? L::kRawStages : L::kVStages;
+  constexpr int kLandedK = L::kFp8 ? kRawKFull0 : kKFull0, kLandedV = L::kFp8 ? kRawVFull0 : kVFull0;
+  auto produce = [&](const volatile Part* P, int g, bool k, bool v, uint64_t deadline) -> bool {
     constexpr int kPages = kKeys / 16;
-    const int oob_row = p.num_blocks * p.num_kv_heads * 16;  // a box starting here is all zero fill
+    constexpr uint32_t kBytes = L::kFp8 ? L::kRawTile : L::kTile;  // 128-byte rows, one or two per key
+    const int oob_row = p.num_blocks * p.num_kv_heads * 16;        // a box starting here is all zero fill
     const int npages = (P->ctx + 15) / 16, hk = P->hk, j1 = P->j1;
     const int32_t* bt = p.block_tables + static_cast<int64_t>(P->s) * p.bt_stride;
     int ids[kPages];  // the block's page ids, loaded a block ahead
     auto fetch = [&](int j) {
 #pragma unroll
       for (int i = 0; i < kPages; ++i) ids[i] = j < j1 && j * kPages + i < npages ? bt[j * kPages + i] : -1;
+    };
+    auto fill = [&](const int (&ys)[kPages], const CUtensorMap* map, uint32_t off, int st, int full, int empty, int round) -> bool {
+      if (round > 0 && !mbar_wait_bounded(B(empty), (round - 1) & 1, deadline)) return false;
+      const uint32_t dst = base + off + st * kBytes;
+      mbar_arrive_expect_tx(B(full), kBytes);
+#pragma unroll
+      for (int i = 0; i < kPages; ++i)
+#pragma unroll
+        for (uint32_t u = 0; u < kBytes / kHalf; ++u) tma_load_2d(dst + u * kHalf + i * 2048, map, B(full), u * 64, ys[i]);
+      return true;
     };
     fetch(P->j0);
     for (int j = P->j0; j < j1; ++j, ++g) {
@@ -393,23 +406,27 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         else if (j * kPages + i < npages) atomicOr(p.err, 1u);
       }
       fetch(j + 1);
-      const int st = g % ns;
-      if (g >= ns && !mbar_wait_bounded(B(empty0 + st), ((g / ns) - 1) & 1, deadline)) return false;
-      constexpr uint32_t kBytes = L::kFp8 ? L::kRawTile : L::kTile;  // 128-byte rows, one or two per key
-      const uint32_t dst = base + off + st * kBytes;
-      mbar_arrive_expect_tx(B(full0 + st), kBytes);
-#pragma unroll
-      for (int i = 0; i < kPages; ++i)
-#pragma unroll
-        for (uint32_t u = 0; u < kBytes / kHalf; ++u)
-          tma_load_2d(dst + u * kHalf + i * 2048, map, B(full0 + st), u * 64, ys[i]);
-      ++issued;
+      if (k) {
+        const int st = g % kRingK;
+        if (!fill(ys, &kmap, L::kFp8 ? L::kRawKOff : L::kKOff, st, kLandedK + st, (L::kFp8 ? kRawKEmpty0 : kKEmpty0) + st,
+                  g / kRingK))
+          return false;
+        ++issued_k;
+      }
+      if (v) {
+        const int st = g % kRingV;
+        if (!fill(ys, &vmap, L::kFp8 ? L::kRawVOff : L::kVOff, st, kLandedV + st, (L::kFp8 ? kRawVEmpty0 : kVEmpty0) + st,
+                  g / kRingV))
+          return false;
+        ++issued_v;
+      }
     }
     return true;
   };
 
-  // e4m3: a warp widens one ring's pages into its operand tiles, exactly (every code is an f16).
-  auto widen_all = [&](uint32_t raw_off, int raw_full0, int raw_empty0, uint32_t off, int ns, int full0, int empty0) {
+  // e4m3: two warps widen one ring's pages into its operand tiles (warp `half` the tile's rows 32 half and
+  // on), exactly: every code is an f16.
+  auto widen_all = [&](int half, uint32_t raw_off, int raw_full0, int raw_empty0, uint32_t off, int ns, int full0, int empty0) {
     // 16 codes at a time: chunk c of a row becomes chunks 2c and 2c + 1 of the widened one. Of eight
     // lanes, four read a row's first half and four its neighbour's second half, so that neither their
     // loads nor their stores meet on a bank.
@@ -433,8 +450,8 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         }
         const uint32_t raw = base + raw_off + rs * kHalf, dst = base + off + st * L::kTile + dst0;
 #pragma unroll 4
-        for (int i = 0; i < kKeys / 4; ++i) {
-          const int row = ((lane >> 3) + 4 * i) ^ (c >> 2);
+        for (int i = 0; i < kKeys / 8; ++i) {
+          const int row = (32 * half + (lane >> 3) + 4 * i) ^ (c >> 2);
           uint32_t w[4], o[8];
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
@@ -459,15 +476,16 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     if (!ok && lane == 0) atomicOr(p.err, 4u);
   };
 
-  if (warp >= 8) {
+  if (L::kFp8 && (warp >= 8 || warp == 6)) {
     if constexpr (L::kFp8) {
-      if (warp == 8) widen_all(L::kRawKOff, kRawKFull0, kRawKEmpty0, L::kKOff, L::kKStages, kKFull0, kKEmpty0);
-      else widen_all(L::kRawVOff, kRawVFull0, kRawVEmpty0, L::kVOff, L::kVStages, kVFull0, kVEmpty0);
+      if (warp == 8 || warp == 9) widen_all(warp - 8, L::kRawKOff, kRawKFull0, kRawKEmpty0, L::kKOff, L::kKStages, kKFull0, kKEmpty0);
+      else widen_all(warp == 10, L::kRawVOff, kRawVFull0, kRawVEmpty0, L::kVOff, L::kVStages, kVFull0, kVEmpty0);
     }
   } else if (warp == 4) {
-    // ---- TMA producer of K, and the schedule ---------------------------------------------------------
+    // ---- TMA producer of K (e4m3: of both), and the schedule -----------------------------------------
     if (lane == 0) {
       prefetch_tensormap(&kmap);
+      if constexpr (L::kFp8) prefetch_tensormap(&vmap);
       for (int it = 0, g = 0; ok; ++it) {
         const uint64_t deadline = globaltimer_ns() + kWaitNs;
         Part P;
@@ -481,8 +499,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         to->ctx = P.ctx, to->j0 = P.j0, to->j1 = P.j1, to->first = P.first, to->last = P.last;
         mbar_arrive(B(kPartFull0 + it % kParts));
         if (!more) break;
-        if constexpr (L::kFp8) ok = produce(&P, g, &kmap, L::kRawKOff, L::kRawStages, kRawKFull0, kRawKEmpty0, deadline);
-        else ok = produce(&P, g, &kmap, L::kKOff, L::kKStages, kKFull0, kKEmpty0, deadline);
+        ok = produce(&P, g, true, L::kFp8, deadline);
         g += P.j1 - P.j0;
       }
       if (!ok) atomicOr(p.err, 4u);
@@ -496,8 +513,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         const volatile Part* P = take_part(it, deadline);
         ok = P != nullptr;
         if (!ok || P->j0 == P->j1) break;
-        if constexpr (L::kFp8) ok = produce(P, g, &vmap, L::kRawVOff, L::kRawStages, kRawVFull0, kRawVEmpty0, deadline);
-        else ok = produce(P, g, &vmap, L::kVOff, L::kVStages, kVFull0, kVEmpty0, deadline);
+        ok = produce(P, g, false, true, deadline);
         g += P->j1 - P->j0;
         leave_part(it);
       }
@@ -620,8 +636,8 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     // the first half's, are turned by half a tile, so that the two use different quarters of the SM.
     auto turn_of = [&](int rows_left) { return rows_left <= kRows / 2 && blockIdx.x * 2 >= gridDim.x ? kRows / 2 : 0; };
     // A part's Q rows into the swizzled tile, as asynchronous copies of 16-byte chunks, a row's by
-    // neighbouring lanes; rows past the last keep what the tile held (each row's products are its own).
-    // start_q may run once the QKs of the part before have (this warp has seen its last S), finish_q
+    // neighbouring lanes; rows past the last are zero (each row's products are its own, but zeros cost
+    // the tensor cores less power, and these kernels run into the GPU's power limit). start_q may run once the QKs of the part before have (this warp has seen its last S), finish_q
     // hands the tile to the QK issuer.
     constexpr int kRowChunks = D / 8;
     auto q_addr = [&](int x) -> uint32_t {
@@ -635,7 +651,10 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
 #pragma unroll 4
       for (int x = lane; x < 32 * kRowChunks; x += 32) {
         const int row = from + x / kRowChunks;
-        if (row >= left) break;
+        if (row >= left) {
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(q_addr(x)), "r"(0u) : "memory");
+          continue;
+        }
         const int R = row0 + row, node = div_group(R, inv_g);
         const uint16_t* src = q0 + node * p.q_stride_t + (head0 + R - node * G) * p.q_stride_h;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(q_addr(x)), "l"(src) : "memory");
@@ -695,7 +714,8 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
           asm volatile("prefetch.global.L1 [%0];" ::"l"(words));
         }
       }
-      float m = -INFINITY, l = 0.f;  // m: the reference P and l are taken against (lazily raised)
+      // m: the reference P and l are taken against (lazily raised); past the last row, P is 0 against it.
+      float m = valid ? -INFINITY : INFINITY, l = 0.f;
       // Block j's P from its S. kMasked: some row may not see all of its keys.
       auto softmax = [&](auto masked_tag, int j) -> bool {
         constexpr bool kMasked = decltype(masked_tag)::value;
@@ -772,7 +792,8 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         return true;
       };
       auto got_s = [&](int gb) -> bool {
-        const bool got = mbar_wait_bounded_poll(B(kSFull0 + (gb & 1)), (gb >> 1) & 1, deadline);
+        const bool got = working ? mbar_wait_bounded_poll(B(kSFull0 + (gb & 1)), (gb >> 1) & 1, deadline)
+                                 : mbar_wait_bounded(B(kSFull0 + (gb & 1)), (gb >> 1) & 1, deadline);
         if (!__all_sync(kFull, got)) return false;
         tc05::fence_after_sync();
         return true;
@@ -812,7 +833,12 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         // holds infinities or NaN: rows behind the context are zeroed, and a node's non-finite elements
         // too, the node noted for the epilogue, which gives them to the rows that do see it.
         if (j >= j_mask) {
-          const bool landed = mbar_wait_bounded(B(kVFull0 + gb % L::kVStages), (gb / L::kVStages) & 1, deadline);
+          // With one V stage the barrier may still lie in block gb - 1's phase, whose predecessor has the
+          // parity waited for: P.V(gb - 1) must have run first. (With more, S(gb) says that P.V(gb - 2)
+          // has, so the stage's barrier lies in block gb's phase.)
+          bool landed = L::kVStages > 1 || gb == 0 ||
+                        mbar_wait_bounded(B(kODone0 + ((gb - 1) & 1)), ((gb - 1) >> 1) & 1, deadline);
+          landed = landed && mbar_wait_bounded(B(kVFull0 + gb % L::kVStages), (gb / L::kVStages) & 1, deadline);
           if (!__all_sync(kFull, landed)) {
             ok = false;
             break;
@@ -947,11 +973,11 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
   if (any_fail && (warp == 4 || warp == 6) && lane == 0) {
     // A wait gave up, so copies in flight may not have been consumed: give them a bounded chance to land
     // before the shared memory goes. Only the last fill of each stage can be outstanding.
-    const int ns = L::kFp8 ? L::kRawStages : (warp == 4 ? L::kKStages : L::kVStages);
-    const int full0 = warp == 4 ? (L::kFp8 ? kRawKFull0 : kKFull0) : (L::kFp8 ? kRawVFull0 : kVFull0);
     const uint64_t drain_deadline = globaltimer_ns() + 100000000ull;
-    for (int j = max(0, issued - ns); j < issued; ++j)
-      mbar_wait_bounded(B(full0 + j % ns), (j / ns) & 1, drain_deadline);
+    for (int j = max(0, issued_k - kRingK); j < issued_k; ++j)
+      mbar_wait_bounded(B(kLandedK + j % kRingK), (j / kRingK) & 1, drain_deadline);
+    for (int j = max(0, issued_v - kRingV); j < issued_v; ++j)
+      mbar_wait_bounded(B(kLandedV + j % kRingV), (j / kRingV) & 1, drain_deadline);
   }
 }
 
