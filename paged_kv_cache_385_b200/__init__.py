@@ -17,6 +17,11 @@ from typing import Optional, Sequence
 
 import torch
 
+try:
+    from . import _views
+except ImportError as e:
+    raise ImportError("the _views module is not built; run `python paged_kv_cache_385_b200/build.py`") from e
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # PAGED_KV_CACHE_LIB points the binding at another build of the library (e.g. a tuning variant).
 LIB_PATH = os.environ.get("PAGED_KV_CACHE_LIB") or os.path.join(_HERE, "libpagedattn.so")
@@ -98,11 +103,10 @@ def _load() -> ctypes.CDLL:
         "pa_rope_opts_init": (None, [ctypes.POINTER(PaRopeOpts)]),
         "pa_rope_inv_freq": (ctypes.c_int, [ctypes.POINTER(F32), I32, ctypes.c_double, I32, ctypes.c_double, I64,
                                             ctypes.c_double, ctypes.c_double]),
-        "pa_rope_and_cache": (ctypes.c_int, [P, P, P, P, P, P, P, P, P, ctypes.POINTER(PaRopeOpts), VP]),
-        "pa_decode_tree": (ctypes.c_int, [P, P, P, P, P, P, P, P, I32, F32, F32, I32, ctypes.POINTER(PaDecodeOpts),
-                                          VP]),
+        "pa_rope_and_cache": (ctypes.c_int, [VP] * 9 + [ctypes.POINTER(PaRopeOpts), VP]),
+        "pa_decode_tree": (ctypes.c_int, [VP] * 8 + [I32, F32, F32, I32, ctypes.POINTER(PaDecodeOpts), VP]),
         "pa_decode_tree_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32]),
-        "pa_commit_tree": (ctypes.c_int, [P, P, P, P, P, P, P, P, VP, VP]),
+        "pa_commit_tree": (ctypes.c_int, [VP] * 10),
         "pa_decode_no_alloc": (ctypes.c_int, [P, P, P, P, P, P, F32, I32, ctypes.POINTER(PaDecodeOpts), VP]),
         "pa_decode_partition_tokens": (I32, [I32, I32, I32]),
         "pa_decode_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32]),
@@ -172,10 +176,35 @@ def as_pa_tensor(t: Optional[torch.Tensor], name: str, device: bool = True) -> P
 
 def _stream_handle(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+# The current stream's handle without building a torch.cuda.Stream around it (3.1 us a call, against 0.1).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_stream() -> int:
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
+
+
+def _views_of(names: Sequence[str], tensors: tuple, optional: Sequence[str] = ()):
+    """(buffer, addresses) of the pa_tensor views of a call's tensors: None for an absent optional one. Every
+    tensor must be on the current device, whose stream the call goes to. Keep the buffer until the call is made."""
+    device = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    got = _views.pack(tensors, _DTYPES, device)
+    if not isinstance(got, int):
+        for name, t in zip(names, tensors):
+            if t is None and name not in optional:
+                raise ValueError(f"{name} is None")
+        return got
+    t, name = tensors[got], names[got]
+    as_pa_tensor(t, name)  # says what is wrong with it, unless it is the device
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{device}")
 
 
 def pa_reshape_and_cache(key: torch.Tensor, value: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
@@ -286,6 +315,12 @@ def pa_prefill(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cach
                            int(kernel), ctypes.c_void_p(_stream_handle(stream))), "pa_prefill")
 
 
+_ROPE_ARGS = ("q_out", "q", "key", "value", "positions", "inv_freq", "slot_mapping", "k_cache", "v_cache")
+_TREE_ARGS = ("out", "q", "k_cache", "v_cache", "block_tables", "query_start", "context_lens", "tree_mask")
+_COMMIT_ARGS = ("k_cache", "v_cache", "block_tables", "query_start", "context_lens", "accepted", "accepted_lens",
+                "new_context_lens")
+
+
 def _error_word_ptr(error_word: Optional[torch.Tensor]) -> Optional[int]:
     if error_word is None:
         return None
@@ -314,12 +349,9 @@ def pa_rope_and_cache(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], 
     _lib.pa_rope_opts_init(ctypes.byref(o))
     o.interleaved, o.magnitude, o.k_scale, o.v_scale = int(bool(interleaved)), magnitude, k_scale, v_scale
     o.error_word = _error_word_ptr(error_word)
-    qs = [None if t is None else ctypes.byref(as_pa_tensor(t, n)) for t, n in ((q_out, "q_out"), (q, "q"))]
-    args = [as_pa_tensor(key, "key"), as_pa_tensor(value, "value"), as_pa_tensor(positions, "positions"),
-            as_pa_tensor(inv_freq, "inv_freq"), as_pa_tensor(slot_mapping, "slot_mapping"),
-            as_pa_tensor(k_cache, "k_cache"), as_pa_tensor(v_cache, "v_cache")]
-    _check(_lib.pa_rope_and_cache(*qs, *[ctypes.byref(a) for a in args], ctypes.byref(o),
-                                  ctypes.c_void_p(_stream_handle(stream))), "pa_rope_and_cache")
+    keep, refs = _views_of(_ROPE_ARGS, (q_out, q, key, value, positions, inv_freq, slot_mapping, k_cache, v_cache),
+                           ("q_out", "q"))
+    _check(_lib.pa_rope_and_cache(*refs, ctypes.byref(o), _stream_handle(stream)), "pa_rope_and_cache")
 
 
 def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -332,13 +364,10 @@ def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_
         opts = decode_opts(**kw)
     elif kw:
         raise TypeError("pass either opts or keyword options, not both")
-    args = [as_pa_tensor(out, "out"), as_pa_tensor(q, "q"), as_pa_tensor(k_cache, "k_cache"),
-            as_pa_tensor(v_cache, "v_cache"), as_pa_tensor(block_tables, "block_tables"),
-            as_pa_tensor(query_start, "query_start"), as_pa_tensor(context_lens, "context_lens")]
-    mask = None if tree_mask is None else ctypes.byref(as_pa_tensor(tree_mask, "tree_mask"))
-    _check(_lib.pa_decode_tree(*[ctypes.byref(a) for a in args], mask, int(max_query_len), float(scale),
-                               float(softcap), int(num_kv_heads), ctypes.byref(opts),
-                               ctypes.c_void_p(_stream_handle(stream))), "pa_decode_tree")
+    keep, refs = _views_of(_TREE_ARGS, (out, q, k_cache, v_cache, block_tables, query_start, context_lens, tree_mask),
+                           ("tree_mask",))
+    _check(_lib.pa_decode_tree(*refs, int(max_query_len), float(scale), float(softcap), int(num_kv_heads),
+                               ctypes.byref(opts), _stream_handle(stream)), "pa_decode_tree")
 
 
 def pa_decode_tree_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -352,13 +381,9 @@ def pa_commit_tree(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: t
                    accepted_lens: torch.Tensor, new_context_lens: Optional[torch.Tensor] = None,
                    error_word: Optional[torch.Tensor] = None, stream=None) -> None:
     """Move each sequence's accepted path to the front of its drafted region (see include/pa.h)."""
-    args = [as_pa_tensor(k_cache, "k_cache"), as_pa_tensor(v_cache, "v_cache"),
-            as_pa_tensor(block_tables, "block_tables"), as_pa_tensor(query_start, "query_start"),
-            as_pa_tensor(context_lens, "context_lens"), as_pa_tensor(accepted, "accepted"),
-            as_pa_tensor(accepted_lens, "accepted_lens")]
-    new = None if new_context_lens is None else ctypes.byref(as_pa_tensor(new_context_lens, "new_context_lens"))
-    _check(_lib.pa_commit_tree(*[ctypes.byref(a) for a in args], new, ctypes.c_void_p(_error_word_ptr(error_word)),
-                               ctypes.c_void_p(_stream_handle(stream))), "pa_commit_tree")
+    keep, refs = _views_of(_COMMIT_ARGS, (k_cache, v_cache, block_tables, query_start, context_lens, accepted,
+                                          accepted_lens, new_context_lens), ("new_context_lens",))
+    _check(_lib.pa_commit_tree(*refs, _error_word_ptr(error_word), _stream_handle(stream)), "pa_commit_tree")
 
 
 def pa_selftest_bounded_wait(timeout_us: int, error_word: Optional[torch.Tensor] = None, stream=None) -> None:

@@ -1,4 +1,5 @@
-"""Build libpagedattn.so in-tree with nvcc for sm_100a (no GPU needed: nvcc cross-compiles).
+"""Build libpagedattn.so in-tree with nvcc for sm_100a (no GPU needed: nvcc cross-compiles), and the
+binding's ``_views`` extension module with gcc.
 
     python paged_kv_cache_385_b200/build.py [--force] [--verbose] [--ptxas-v]
 
@@ -16,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,6 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedattn.so")
+VIEWS_SOURCE = os.path.join(CSRC, "views.c")  # the binding's tensor marshalling, a CPython extension module
+VIEWS = os.path.join(PKG, "_views" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 SOURCES = ["api.cu", "decode.cu", "decode_units.cu", "multiquery.cu", "prefill_tc.cu", "tree.cu", "tree_commit.cu",
            "rope.cu", "cache.cu", "no_alloc.cu", "selftest.cu", "allocator.cpp"]
@@ -39,16 +43,16 @@ def nvcc() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES]
+    files = [os.path.join(CSRC, s) for s in SOURCES] + [VIEWS_SOURCE]
     for d in (CSRC, INCLUDE):
         files += [os.path.join(d, f) for f in os.listdir(d) if f.endswith((".h", ".cuh"))]
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(VIEWS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(VIEWS))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -65,6 +69,18 @@ def _compile(src: str, verbose: bool, extra) -> str:
     return obj
 
 
+def _build_views(verbose: bool) -> None:
+    tmp = VIEWS + ".tmp"
+    cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"], "-I" + INCLUDE, VIEWS_SOURCE,
+           "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on {VIEWS_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, VIEWS)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile every source for sm_100a and link libpagedattn.so; returns its path."""
     if not force and up_to_date():
@@ -79,6 +95,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _build_views(verbose)
     os.replace(tmp, LIB)
     return LIB
 

@@ -322,6 +322,27 @@ def test_binding_refuses_host_tensors():
         pa.pa_decode_tree(*list(t.values()), 5, 0.1, 2, opts=pa.PaDecodeOpts(), k_scale=1.0)
     with pytest.raises(ValueError, match="CUDA"):
         pa.pa_commit_tree(*commit_args().values())
+    for call, a, name in ((pa.pa_rope_and_cache, rope_args(key=None), "key"), (pa.pa_commit_tree, commit_args(lens=None), "context_lens")):
+        with pytest.raises(ValueError, match="CUDA|" + name):
+            call(*a.values())
+
+
+def test_views_of_tensors():
+    """The extension's views are as_pa_tensor's, field by field; what is no view is named by its place."""
+    ts = (torch.zeros(3, 4, 8)[:, 1:3], None, torch.zeros(5, dtype=I64), torch.zeros(0, 2, dtype=BF), torch.tensor(1, dtype=I32),
+          torch.zeros(2, 3, 4, 5, dtype=F16).permute(3, 0, 2, 1), torch.zeros(2, 6, dtype=E4))
+    keep, refs_ = pa._views.pack(ts, pa._DTYPES, -1)
+    assert refs_[1] is None and len(refs_) == len(ts)
+    for t, at in zip(ts, refs_):
+        if t is not None:
+            got, want = pa.PaTensor.from_address(at), pa.as_pa_tensor(t, "t", device=False)
+            assert bytes(got) == bytes(want)
+    assert pa._views.pack((ts[0], torch.zeros(1, dtype=torch.uint8)), pa._DTYPES, -1) == 1
+    assert pa._views.pack((torch.zeros(1, 1, 1, 1, 1),), pa._DTYPES, -1) == 0
+    assert pa._views.pack((ts[0],), pa._DTYPES, 0) == 0  # on another device
+    for bad in ((None, pa._DTYPES, 0), ((3,), pa._DTYPES, 0), ((ts[0],), [], 0), ((ts[0],), pa._DTYPES, "0")):
+        with pytest.raises((TypeError, AttributeError)):
+            pa._views.pack(*bad)
 
 
 # ---- the oracle's own pins -------------------------------------------------------------------------
