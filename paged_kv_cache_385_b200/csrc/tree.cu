@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kRows = 128;  // query rows of an item
 constexpr int kKeys = 64;   // keys of a block
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 8;
 constexpr int kWhole = 4;
 constexpr int kMinSpan = 6;
 constexpr uint32_t kQHalf = kRows * 128;  // a 64-element (128-byte) column half of the Q tile

@@ -19,7 +19,7 @@ namespace pa {
 namespace {
 
 constexpr int kCommitThreads = 256;
-constexpr int kCommitChunks = 8;  // 16-byte chunks a thread holds between reading and writing
+constexpr int kCommitChunks = 4;  // 16-byte chunks a thread holds between reading and writing
 constexpr int kCommitCtas = 4 * 148;
 
 __global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(const CommitParams p) {
@@ -65,32 +65,40 @@ __global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(const Commi
   }
   if (!good) return;
 
-  // Chunk x of this CTA: (pool, path node, 16 bytes of the row), path nodes ascending within a pool.
-  const int pools = 2 * p.num_kv_heads, chunks = p.row_bytes / 16, per_pool = (taken - kept) * chunks;
+  // A thread carries the same chunk (16 bytes of a path node's row) of every pool that it takes: of
+  // pools pool0 + l, pool0 + l + lanes, ... Chunks go up with the path, kCommitThreads at a time.
+  const int pools = 2 * p.num_kv_heads, chunks = p.row_bytes / 16, total = (taken - kept) * chunks;
   const int pool0 = static_cast<int>(static_cast<int64_t>(pools) * blockIdx.y / gridDim.y);
   const int pool1 = static_cast<int>(static_cast<int64_t>(pools) * (blockIdx.y + 1) / gridDim.y);
-  const int64_t total = static_cast<int64_t>(pool1 - pool0) * per_pool;
-  for (int64_t base = 0; base < total; base += kCommitThreads * kCommitChunks) {
-    uint4 v[kCommitChunks];
-    uint4* dst[kCommitChunks];
-#pragma unroll
-    for (int k = 0; k < kCommitChunks; ++k) {
-      const int64_t x = base + k * kCommitThreads + threadIdx.x;
-      dst[k] = nullptr;
-      if (x >= total) continue;
-      const int pool = static_cast<int>(x / per_pool), y = static_cast<int>(x - static_cast<int64_t>(pool) * per_pool);
-      const int i = kept + y / chunks, c = y % chunks;
-      const int hk = (pool0 + pool) >> 1;
-      uint8_t* rows = static_cast<uint8_t*>((pool0 + pool) & 1 ? p.v_cache : p.k_cache);
-      const int64_t a = from[i], b = to[i];
-      if (a < 0 || b < 0) continue;
-      v[k] = *reinterpret_cast<const uint4*>(rows + (a + hk * 16) * p.row_bytes + c * 16);
-      dst[k] = reinterpret_cast<uint4*>(rows + (b + hk * 16) * p.row_bytes + c * 16);
+  const int span = min(total, kCommitThreads);
+  for (int x0 = 0; x0 < total; x0 += span) {
+    const int lanes = kCommitThreads / span, l = threadIdx.x / span, x = x0 + static_cast<int>(threadIdx.x) - l * span;
+    int64_t a = -1, b = -1;
+    if (l < lanes && x < total) {
+      const int i = kept + x / chunks, c = x % chunks;
+      if (from[i] >= 0 && to[i] >= 0) {
+        a = from[i] * p.row_bytes + c * 16;
+        b = to[i] * p.row_bytes + c * 16;
+      }
     }
-    __syncthreads();  // the group's rows are read before any of it is written
+    const int64_t head_bytes = static_cast<int64_t>(16) * p.row_bytes;
+    for (int first = pool0 + l; first - l < pool1; first += lanes * kCommitChunks) {
+      uint4 v[kCommitChunks];
 #pragma unroll
-    for (int k = 0; k < kCommitChunks; ++k)
-      if (dst[k]) *dst[k] = v[k];
+      for (int k = 0; k < kCommitChunks; ++k) {
+        const int pool = first + k * lanes;
+        if (a >= 0 && pool < pool1)
+          v[k] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool & 1 ? p.v_cache : p.k_cache) +
+                                                 (pool >> 1) * head_bytes + a);
+      }
+      __syncthreads();  // these pools' rows are read before any of them is written
+#pragma unroll
+      for (int k = 0; k < kCommitChunks; ++k) {
+        const int pool = first + k * lanes;
+        if (a >= 0 && pool < pool1)
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(pool & 1 ? p.v_cache : p.k_cache) + (pool >> 1) * head_bytes + b) = v[k];
+      }
+    }
   }
 }
 
