@@ -28,7 +28,7 @@ LIB = os.path.join(PKG, "libpagedattn.so")
 VIEWS_SOURCE = os.path.join(CSRC, "views.c")  # the binding's tensor marshalling, a CPython extension module
 VIEWS = os.path.join(PKG, "_views" + sysconfig.get_config_var("EXT_SUFFIX"))
 
-SOURCES = ["api.cu", "decode.cu", "decode_units.cu", "multiquery.cu", "prefill_tc.cu", "tree.cu", "tree_commit.cu",
+SOURCES = ["api.cu", "decode.cu", "decode_units.cu", "multiquery.cu", "prefill_tc.cu", "tree.cu", "tree_few.cu", "tree_commit.cu",
            "rope.cu", "cache.cu", "no_alloc.cu", "selftest.cu", "allocator.cpp"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I" + INCLUDE, "-I" + CSRC,

@@ -245,13 +245,14 @@ size_t workspace_layout(int64_t B, int64_t Hq, int64_t D, int64_t P, size_t* ml_
 
 // Layout of the tree workspace: partial rows, then their (m, l), then a descriptor per span. 0 bytes when
 // no context can be cut.
-size_t tree_workspace(int64_t head_dim, int64_t max_ctx, int spans, size_t* ml_offset, size_t* desc_offset) {
-  if (!pa::tree_splits(max_ctx)) return 0;
-  const size_t acc = round_up(static_cast<size_t>(2 * spans) * pa::kTreeRows * static_cast<size_t>(head_dim) * sizeof(float), 256);
-  const size_t ml = round_up(static_cast<size_t>(2 * spans) * pa::kTreeRows * 2 * sizeof(float), 256);
+size_t tree_workspace(int64_t head_dim, const pa::TreePlan& plan, size_t* ml_offset, size_t* desc_offset) {
+  if (!plan.splits) return 0;
+  const size_t rows = static_cast<size_t>(2) * plan.spans * plan.rows;
+  const size_t acc = round_up(rows * static_cast<size_t>(head_dim) * sizeof(float), 256);
+  const size_t ml = round_up(rows * 2 * sizeof(float), 256);
   if (ml_offset) *ml_offset = acc;
   if (desc_offset) *desc_offset = acc + ml;
-  return acc + ml + round_up(static_cast<size_t>(spans) * pa::kTreeDescInts * sizeof(int32_t), 256);
+  return acc + ml + round_up(static_cast<size_t>(plan.spans) * pa::kTreeDescInts * sizeof(int32_t), 256);
 }
 
 }  // namespace
@@ -1012,8 +1013,7 @@ size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int
   if (num_seqs <= 0 || num_kv_heads <= 0 || num_q_heads < num_kv_heads || head_dim <= 0 || max_query_len <= 0 ||
       max_context_len <= 0)
     return 0;
-  return tree_workspace(head_dim, max_context_len,
-                        pa::tree_spans(num_seqs, num_kv_heads, num_q_heads / num_kv_heads, max_query_len, max_context_len),
+  return tree_workspace(head_dim, pa::tree_plan(num_seqs, num_kv_heads, num_q_heads / num_kv_heads, max_query_len, max_context_len),
                         nullptr, nullptr);
 }
 
@@ -1128,9 +1128,10 @@ int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache,
   p.score_scale = scale * k_scale;
   p.softcap = softcap;
   p.v_scale = v_scale;
-  p.spans = pa::tree_spans(B, num_kv_heads, p.group, max_query_len, max_ctx);
+  const pa::TreePlan plan = pa::tree_plan(B, num_kv_heads, p.group, max_query_len, max_ctx);
+  p.spans = plan.spans;
   size_t ml_off = 0, desc_off = 0;
-  if (const size_t need = tree_workspace(D, max_ctx, p.spans, &ml_off, &desc_off)) {
+  if (const size_t need = tree_workspace(D, plan, &ml_off, &desc_off)) {
     const size_t have = opts.workspace ? opts.workspace_bytes : 0;
     if (have < need)
       return fail(PA_ERR_WORKSPACE, "contexts of up to %lld tokens need a workspace of %zu bytes (got %zu)", (long long)max_ctx,

@@ -197,11 +197,11 @@ struct TreeParams {
   float score_scale;  // scale * k_scale
   float softcap;      // 0 = none
   float v_scale;
-  int32_t spans;  // CTAs (each takes an equal span of the batch's key blocks)
+  int32_t spans;  // workers (CTAs or warps), each with an equal span of the batch's keys
   // Rows of items that spans cut; all null when no context can be cut. Span c owns slots 2 c (its first
   // item, begun in an earlier span) and 2 c + 1 (its last, ended in a later one).
-  float* ws_acc;     // [2 spans][D / 4][128 rows][4]
-  float2* ws_ml;     // [2 spans][128]: running maximum (log2 units) and sum
+  float* ws_acc;     // [2 spans][D / 4][rows of a tile][4]
+  float2* ws_ml;     // [2 spans][rows of a tile]: running maximum (log2 units) and sum
   int32_t* ws_desc;  // [spans][kTreeDescInts]: q row, tile, KV head, rows and parts of the item begun there
   uint32_t* err;
 };
@@ -209,10 +209,20 @@ constexpr int kTreeMaxNodes = 256;
 constexpr int kTreeMaskWords = kTreeMaxNodes / 64;
 constexpr int kTreeMaxSpans = 2 * 148;  // two CTAs per SM
 constexpr int kTreeDescInts = 8;
-constexpr int kTreeRows = 128;
+constexpr int kTreeRows = 128;    // rows of a tile: tcgen05 kernel,
+constexpr int kTreeFewRows = 16;  // and warp-level kernel, which takes batches of at most so many rows
+constexpr int kTreeFewOcc1 = 3, kTreeFewOcc2 = 2;  // its CTAs per SM with up to 8 rows, and with more
 bool tree_supported(KvType kv, int head_dim, int group);
-bool tree_splits(int64_t max_context_len);  // whether a context of that length may be cut
-int tree_spans(int64_t num_seqs, int num_kv_heads, int group, int max_query_len, int64_t max_context_len);
+// How a batch of these sizes is worked on: rows of a tile, spans, and whether a context may be cut.
+struct TreePlan {
+  int rows, spans;
+  bool splits;
+};
+TreePlan tree_plan(int64_t num_seqs, int num_kv_heads, int group, int max_query_len, int64_t max_context_len);
+bool tree_few_splits(int64_t max_context_len);
+int tree_few_spans(int64_t num_seqs, int num_kv_heads, int rows, int64_t max_context_len);
+cudaError_t launch_decode_tree_few(KvType kv, QType q, int head_dim, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                                   const TreeParams& p, cudaStream_t stream);
 cudaError_t launch_decode_tree(KvType kv, QType q, int head_dim, const CUtensorMap& k_map, const CUtensorMap& v_map,
                                const TreeParams& p, cudaStream_t stream);
 

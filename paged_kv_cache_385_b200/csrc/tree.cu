@@ -5,12 +5,8 @@
 // the keys with a running maximum and sum. A mask touches only the keys past `start`, at most five key
 // blocks at the end of a context: every other block is a dense product.
 //
-// Work. An item is a tile of up to 128 rows of one (sequence, KV head); 64 keys (4 pages) are a block.
-// The batch's items, laid end to end with kItemCost blocks' worth of fixed cost before each, are cut
-// into gridDim.x equal spans, so every CTA streams the same number of blocks whatever the lengths are:
-// a span's first and last items may be parts of items, whose unnormalised rows go to the workspace and
-// are joined by merge_kernel. Items of at most kWhole blocks are never cut. The cuts depend on lengths
-// alone, and partial rows are joined in span order, so results do not depend on timing or placement.
+// Work. An item is a tile of up to 128 rows of one (sequence, KV head), a unit of it 64 keys (4 pages): the
+// equal spans of tree_sched.cuh, one to each of two CTAs per SM. At most 16 rows: tree_few.cu.
 //
 // Per block, as in the prefill kernel: S = Q K^T (tcgen05, K-major operands in 128-byte-swizzled shared
 // memory, two S buffers in tensor memory), softmax by 4 warps with a row per thread, P over S in tensor
@@ -24,15 +20,17 @@
 #include "internal.h"
 #include "pa_device.cuh"
 #include "tc05.cuh"
+#include "tree_sched.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kRows = 128;  // query rows of an item
+constexpr int kRows = kTreeRows;  // query rows of an item
 constexpr int kKeys = 64;   // keys of a block
-constexpr int kItemCost = 8;
-constexpr int kWhole = 4;
-constexpr int kMinSpan = 6;
+using Pol = tree::Policy<kKeys, kRows, 8, 4, 6>;  // units are blocks
+using tree::Part;
+using tree::visible_bits;
+constexpr int kParts = 4;  // parts handed on and not yet left by every role
 constexpr uint32_t kQHalf = kRows * 128;  // a 64-element (128-byte) column half of the Q tile
 constexpr uint32_t kHalf = kKeys * 128;   // of a K or V tile
 // O is rescaled only when a row's maximum grows by more than this (log2 units): until then P and the
@@ -69,16 +67,6 @@ struct Layout {
 };
 constexpr uint32_t kTmemCols = 256;  // two S buffers of kKeys columns, then O's D columns
 
-// A CTA's part of an item, as the K producer hands it to the other roles through shared memory.
-struct alignas(16) Part {
-  int s, q0, rows, tile;
-  int hk, start, ctx;
-  int j0, j1;       // its key blocks; none: the span is done
-  int first, last;  // the CTAs that hold the item's first and last blocks
-  int unused;
-};
-constexpr int kParts = 4;  // parts handed on and not yet left by every role
-
 enum {
   kQFull = 0,    // 4 softmax warps: the item's Q tile is in place
   kKFull0 = 1,   // up to 4
@@ -103,99 +91,6 @@ enum {
 };
 static_assert(kPartFull0 + kParts <= kPartEmpty0 && kPartEmpty0 + kParts <= kPart0, "barrier slots");
 static_assert(sizeof(Part) == 48 && 8 * kPart0 % 16 == 0 && 8 * kPart0 + kParts * sizeof(Part) <= kBarBytes, "barrier area");
-
-// ---- the schedule -------------------------------------------------------------------------------
-
-struct Seq {
-  int q0, n, ctx, rows, tiles, nkb;
-};
-
-// Sequence s, with no tiles when it has no nodes or is out of contract (*bad).
-__device__ __forceinline__ Seq load_seq(const TreeParams& p, int s, bool* bad) {
-  Seq q;
-  q.q0 = p.query_start[s];
-  const int64_t n = static_cast<int64_t>(p.query_start[s + 1]) - q.q0;
-  q.ctx = p.context_lens[s];
-  *bad = n < 0 || n > p.max_query_len || n > q.ctx || q.ctx > p.max_context_len || q.q0 < 0 || q.q0 > p.num_tokens - n;
-  q.n = *bad ? 0 : static_cast<int>(n);
-  q.rows = q.n * p.group;
-  q.tiles = (q.rows + kRows - 1) / kRows;
-  q.nkb = q.n ? (q.ctx + kKeys - 1) / kKeys : 0;
-  return q;
-}
-
-__device__ __forceinline__ int64_t seq_cost(const TreeParams& p, const Seq& q) {
-  return static_cast<int64_t>(q.tiles) * p.num_kv_heads * (q.nkb + kItemCost);
-}
-
-// Walks a CTA's span [beg, end) of the items laid end to end.
-struct Cursor {
-  int64_t beg, end, len;  // span, and the spans' common length
-  int64_t at;             // cost before the current item
-  int s, hk, tile;
-  Seq q;
-
-  __device__ __forceinline__ void skip_empty(const TreeParams& p) {
-    bool bad;
-    while (s < p.num_seqs && (q = load_seq(p, s, &bad)).tiles == 0) ++s;
-  }
-  __device__ __forceinline__ bool next(const TreeParams& p, Part* part) {
-    while (s < p.num_seqs && at < end) {
-      const int cost = q.nkb + kItemCost;
-      int64_t j0 = beg - at - kItemCost, j1 = end - at - kItemCost;  // the span, in this item's blocks
-      int first, last;
-      if (q.nkb <= kWhole) {  // whole, where its first block lies
-        const bool mine = j0 <= 0 && j1 > 0;
-        j0 = 0;
-        j1 = mine ? q.nkb : 0;
-        first = last = blockIdx.x;
-      } else {
-        j0 = max(j0, static_cast<int64_t>(0));
-        j1 = min(j1, static_cast<int64_t>(q.nkb));
-        first = static_cast<int>((at + kItemCost) / len);
-        last = static_cast<int>((at + cost - 1) / len);
-      }
-      if (j0 < j1) {
-        part->s = s, part->q0 = q.q0, part->rows = q.rows, part->tile = tile;
-        part->hk = hk, part->start = q.ctx - q.n, part->ctx = q.ctx;
-        part->j0 = static_cast<int>(j0), part->j1 = static_cast<int>(j1);
-        part->first = first, part->last = last;
-      }
-      at += cost;
-      if (++tile == q.tiles) {
-        tile = 0;
-        if (++hk == p.num_kv_heads) {
-          hk = 0;
-          ++s;
-          skip_empty(p);
-        }
-      }
-      if (j0 < j1) return true;
-    }
-    part->j0 = part->j1 = 0;
-    return false;
-  }
-};
-
-// The keys of block t0 .. t0 + 63 that a node sees, as bits.
-__device__ __forceinline__ uint64_t low_ones(int n) { return n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1); }
-__device__ __forceinline__ uint64_t visible_bits(const TreeParams& p, const volatile Part* P, int node, int t0) {
-  uint64_t v;
-  if (!p.mask) {
-    v = low_ones(P->start + node + 1 - t0);
-  } else {
-    const uint64_t* row = p.mask + static_cast<int64_t>(P->q0 + node) * p.mask_words;
-    const int o = t0 - P->start;
-    if (o < 0) {
-      v = low_ones(-o) | (o > -64 ? row[0] << -o : 0ull);
-    } else {
-      const int w = o >> 6, sh = o & 63;
-      v = w < p.mask_words ? row[w] >> sh : 0ull;
-      if (sh && w + 1 < p.mask_words) v |= row[w + 1] << (64 - sh);
-    }
-  }
-  return v & low_ones(P->ctx - t0);
-}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
@@ -235,12 +130,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // R / G for R < 4096 and G <= 16, by a multiplication: inv_g = ceil(65536 / G).
 __device__ __forceinline__ int div_group(int R, uint32_t inv_g) { return static_cast<int>((R * inv_g) >> 16); }
 
@@ -260,64 +149,15 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
   auto B = [&](int i) { return bar + 8u * i; };
   pdl_wait();
 
-  // ---- this CTA's span: cost before each thread's share of the sequences ------------------------
-  Cursor cur;
+  // ---- this CTA's span ------------------------------------------------------------------------------
+  tree::Cursor<Pol> cur;
   {
-    constexpr int T = L::kThreads;
-    int64_t* before = reinterpret_cast<int64_t*>(smem);  // [T + 1], in the ring before it is used
-    const int per = (p.num_seqs + T - 1) / T;
-    const int s0 = min(static_cast<int>(threadIdx.x) * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
-    int64_t mine = 0;
-    bool any_bad = false;
-    for (int s = s0; s < s1; ++s) {
-      bool bad;
-      mine += seq_cost(p, load_seq(p, s, &bad));
-      any_bad |= bad;
-    }
-    if (any_bad && blockIdx.x == 0) atomicOr(p.err, 8u);
-    int64_t incl = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t v = __shfl_up_sync(kFull, incl, off);
-      if (lane >= off) incl += v;
-    }
-    int64_t* totals = before + T + 1;  // one per warp
-    if (lane == 31) totals[warp] = incl;
-    __syncthreads();
-    int64_t base_cost = 0;
-    for (int w = 0; w < warp; ++w) base_cost += totals[w];
-    before[threadIdx.x] = base_cost + incl - mine;
-    if (threadIdx.x == T - 1) before[T] = base_cost + incl;
-    __syncthreads();
-    const int64_t total = before[T];
-    cur.len = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kMinSpan));
-    cur.beg = cur.len * blockIdx.x;
-    cur.end = min(cur.beg + cur.len, total);
-    if (cur.beg >= total) {
-      if (threadIdx.x == 0 && p.ws_desc) p.ws_desc[blockIdx.x * kTreeDescInts + 4] = 0;
+    int64_t* before = reinterpret_cast<int64_t*>(smem);  // in the ring before it is used
+    tree::sum_costs<Pol, L::kThreads>(p, before);
+    if (!cur.start<L::kThreads>(p, before, blockIdx.x, gridDim.x)) {
+      if (threadIdx.x == 0) tree::describe_none(p, blockIdx.x);
       return;
     }
-    int lo = 0, hi = T - 1;  // the last share that starts at or before the span
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (before[mid] <= cur.beg) lo = mid;
-      else hi = mid - 1;
-    }
-    cur.at = before[lo];
-    cur.s = min(lo * per, p.num_seqs);
-    cur.hk = cur.tile = 0;
-    cur.skip_empty(p);
-    while (cur.s < p.num_seqs && cur.at + seq_cost(p, cur.q) <= cur.beg) {
-      cur.at += seq_cost(p, cur.q);
-      ++cur.s;
-      cur.skip_empty(p);
-    }
-    // The item of that sequence in which the span begins.
-    const int cost = cur.q.nkb + kItemCost;
-    const int item = static_cast<int>((cur.beg - cur.at) / cost);
-    cur.at += static_cast<int64_t>(item) * cost;
-    cur.hk = item / cur.q.tiles;
-    cur.tile = item % cur.q.tiles;
   }
   __syncthreads();  // the shares are read: the ring may be written
 
@@ -604,10 +444,10 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     const float cap_u = kCap ? 2.f * sl2 / p.softcap : 0.f;
     volatile uint32_t* bad_nodes = reinterpret_cast<volatile uint32_t*>(smem + L::kBarOff + 8 * kBadNodes);
     int meets = 0, turn = 0;
-    if (threadIdx.x == 0 && p.ws_desc) p.ws_desc[blockIdx.x * kTreeDescInts + 4] = 0;
+    if (threadIdx.x == 0) tree::describe_none(p, blockIdx.x);
 
     auto score = [&](float s) -> float {  // a raw product in log2 units
-      if constexpr (kCap) return fmaf(-2.f * cap2, rcp_approx(1.f + ex2(s * cap_u)), cap2);
+      if constexpr (kCap) return fmaf(-2.f * cap2, tree::rcp_approx(1.f + ex2(s * cap_u)), cap2);
       else return s * sl2;
     };
     // Two weights 2^(score - reference): x is replaced by them.
@@ -616,7 +456,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
       if constexpr (kCap) {
         t = fma2(make_float2(x0, x1), make_float2(cap_u, cap_u), make_float2(0.f, 0.f));
         t = add2(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
-        t = fma2(make_float2(rcp_approx(t.x), rcp_approx(t.y)), make_float2(-2.f * cap2, -2.f * cap2),
+        t = fma2(make_float2(tree::rcp_approx(t.x), tree::rcp_approx(t.y)), make_float2(-2.f * cap2, -2.f * cap2),
                  make_float2(cap2 + nref, cap2 + nref));
       } else {
         t = fma2(make_float2(x0, x1), make_float2(sl2, sl2), make_float2(nref, nref));
@@ -934,25 +774,15 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
               *reinterpret_cast<uint4*>(dst + c * 32 + 8 * q) = o;
             }
           } else if (valid) {
-            // Partial rows: four columns of the tile's 128 rows together, so that a warp's stores and
-            // the merge's loads are whole lines.
-            float4* ws = reinterpret_cast<float4*>(p.ws_acc) + static_cast<int64_t>(slot) * (D / 4) * kRows + r;
+            float4* ws = reinterpret_cast<float4*>(p.ws_acc) + tree::ws_at<kRows, D>(slot, 8 * c, r);
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              ws[(8 * c + q) * kRows] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            for (int q = 0; q < 8; ++q) ws[q * kRows] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
           }
           __syncwarp();  // the tensor-memory load above is the whole warp's
         }
         if (valid && !whole) p.ws_ml[slot * kRows + r] = make_float2(m, l);
       }
-      if (threadIdx.x == 0 && !whole && first == static_cast<int>(blockIdx.x)) {
-        int32_t* d = p.ws_desc + blockIdx.x * kTreeDescInts;
-        d[0] = P->q0;
-        d[1] = P->tile;
-        d[2] = P->hk;
-        d[3] = P->rows;
-        d[4] = P->last - first + 1;
-      }
+      if (threadIdx.x == 0 && !whole && first == static_cast<int>(blockIdx.x)) tree::describe(p, blockIdx.x, P);
       tc05::fence_before_sync();
       __syncwarp();
       if (lane == 0) {
@@ -981,75 +811,15 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
   }
 }
 
-// Joins the parts of the items that spans cut: block (c, y) takes rows 8 y .. 8 y + 7 of the item that
-// begins in span c and ends in a later one.
-template <bool kOutBf16, int D>
-__global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
-  constexpr int V = D / 64;  // float4 columns of a thread
-  pdl_wait();
-  const int c = blockIdx.x;
-  const int32_t* d = p.ws_desc + c * kTreeDescInts;
-  const int parts = d[4];
-  if (parts == 0) return;
-  const int r = blockIdx.y * 8 + (threadIdx.x & 7), col = threadIdx.x >> 3;  // columns col, col + 16 of D / 4
-  const int R = d[1] * kRows + r;
-  if (R >= d[3]) return;
-  auto slot = [&](int k) -> int64_t { return k == 0 ? 2 * c + 1 : 2 * (c + k); };
-  float top = -INFINITY;
-  for (int k = 0; k < parts; ++k) top = fmaxf(top, p.ws_ml[slot(k) * kRows + r].x);
-  const float ref = top == -INFINITY ? 0.f : top;
-  float4 acc[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < parts; ++k) {
-    const float2 ml = p.ws_ml[slot(k) * kRows + r];
-    const float w = ex2(ml.x - ref);
-    l += w * ml.y;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float4 a = reinterpret_cast<const float4*>(p.ws_acc)[(slot(k) * (D / 4) + col + 16 * v) * kRows + r];
-      acc[v].x += w * a.x;
-      acc[v].y += w * a.y;
-      acc[v].z += w * a.z;
-      acc[v].w += w * a.w;
-    }
-  }
-  const float inv = l == 0.f ? 0.f : p.v_scale / l;
-  const int node = R / p.group;
-  uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(d[0] + node) * p.o_stride_t +
-                  static_cast<int64_t>(d[2] * p.group + R - node * p.group) * p.o_stride_h;
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    *reinterpret_cast<uint2*>(out + 4 * (col + 16 * v)) =
-        make_uint2(pack2<kOutBf16>(acc[v].x * inv, acc[v].y * inv), pack2<kOutBf16>(acc[v].z * inv, acc[v].w * inv));
-}
-
-template <typename... KArgs, typename... Args>
-cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <KvType KV, bool kQBf16, int D, bool kCap>
 cudaError_t launch_t(const CUtensorMap& km, const CUtensorMap& vm, const TreeParams& p, cudaStream_t st) {
   using L = Layout<KV, D, kCap>;
   auto kern = tree_kernel<KV, kQBf16, D, kCap>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(kern, dim3(p.spans), L::kThreads, L::kSmemBytes, st, km, vm, p);
+  e = tree::launch_dependent(kern, dim3(p.spans), L::kThreads, L::kSmemBytes, st, km, vm, p);
   if (e != cudaSuccess || !p.ws_desc) return e;
-  return launch_dependent(tree_merge_kernel<kQBf16, D>, dim3(p.spans, kRows / 8), 128, 0, st, p);
+  return tree::launch_dependent(tree::merge_kernel<kQBf16, D, kRows>, dim3(p.spans, kRows / 8), 128, 0, st, p);
 }
 
 template <KvType KV, bool kQBf16, int D>
@@ -1063,18 +833,29 @@ bool tree_supported(KvType kv, int head_dim, int group) {
   return group >= 1 && group <= 16 && (head_dim == 128 || (head_dim == 64 && kv != KvType::E4M3));
 }
 
-bool tree_splits(int64_t max_context_len) { return (max_context_len + kKeys - 1) / kKeys > kWhole; }
+// Few rows to a (sequence, KV head) take the warp-level kernel.
+static bool few(int64_t max_query_len, int group) { return max_query_len * group <= kTreeFewRows; }
 
-int tree_spans(int64_t num_seqs, int num_kv_heads, int group, int max_query_len, int64_t max_context_len) {
+TreePlan tree_plan(int64_t num_seqs, int num_kv_heads, int group, int max_query_len, int64_t max_context_len) {
+  TreePlan plan;
+  plan.rows = few(max_query_len, group) ? kTreeFewRows : kRows;
+  if (plan.rows == kTreeFewRows) {
+    plan.spans = tree_few_spans(num_seqs, num_kv_heads, max_query_len * group, max_context_len);
+    plan.splits = tree_few_splits(max_context_len);
+    return plan;
+  }
   // (Each factor is capped where more cannot matter, so that no product overflows.)
   const auto cap = [](int64_t x) { return std::min<int64_t>(x, 1 << 20); };
   const int64_t items = cap(cap(num_seqs) * num_kv_heads) * cap((static_cast<int64_t>(max_query_len) * group + kRows - 1) / kRows);
-  const int64_t cost = cap(items) * ((max_context_len + kKeys - 1) / kKeys + kItemCost);
-  return static_cast<int>(std::min<int64_t>(kTreeMaxSpans, std::max<int64_t>(1, (cost + kMinSpan - 1) / kMinSpan)));
+  const int64_t blocks = (max_context_len + kKeys - 1) / kKeys, cost = cap(items) * (blocks + Pol::kItemCost);
+  plan.spans = static_cast<int>(std::min<int64_t>(kTreeMaxSpans, std::max<int64_t>(1, (cost + Pol::kMinSpan - 1) / Pol::kMinSpan)));
+  plan.splits = blocks > Pol::kWhole;
+  return plan;
 }
 
 cudaError_t launch_decode_tree(KvType kv, QType q, int head_dim, const CUtensorMap& km, const CUtensorMap& vm,
-                                  const TreeParams& p, cudaStream_t st) {
+                               const TreeParams& p, cudaStream_t st) {
+  if (few(p.max_query_len, p.group)) return launch_decode_tree_few(kv, q, head_dim, km, vm, p, st);
   if (kv == KvType::BF16)
     return head_dim == 128 ? launch_cap<KvType::BF16, true, 128>(km, vm, p, st) : launch_cap<KvType::BF16, true, 64>(km, vm, p, st);
   if (kv == KvType::F16)

@@ -53,6 +53,18 @@ CASES = {
     "long_split": ("bf16", 128, 1, 4, [10], [9001], {}),
     "long_split_e4m3": ("e4m3", 128, 1, 8, [3], [8000], {}),
     "long_split_d64": ("f16", 64, 2, 1, [5, 2], [7000, 33], {}),
+    "few_rows": ("bf16", 128, 2, 4, [4, 1, 3, 0], [400, 1, 33, 9], {}),
+    "few_rows_8": ("f16", 128, 3, 1, [8, 5, 1], [1200, 16, 17], {}),
+    "few_rows_16": ("f16", 128, 2, 1, [16, 9, 15], [16, 1000, 47], {}),
+    "few_rows_chain": ("bf16", 64, 2, 3, [5, 2], [500, 31], {"masks": None}),
+    "few_rows_capped": ("f16", 128, 2, 2, [7, 8], [600, 64], {"softcap": 3.0}),
+    "few_rows_d64": ("f16", 64, 4, 1, [3, 7], [100, 65], {}),
+    "few_rows_e4m3": ("e4m3", 128, 2, 8, [2, 1], [900, 40], {}),
+    "few_rows_e4m3_7": ("e4m3", 128, 1, 7, [1, 1, 1], [1, 320, 2000], {"q": "f16", "softcap": 10.0}),
+    "few_rows_long": ("bf16", 128, 1, 8, [2], [20011], {}),
+    "few_rows_long_e4m3": ("e4m3", 128, 2, 1, [7], [30000], {}),
+    "few_rows_negative": ("f16", 128, 1, 2, [6], [150], {"scale": -0.1}),
+    "few_rows_many": ("bf16", 64, 2, 2, [1, 3, 0, 2] * 60, [300, 3, 5, 70] * 60, {}),
     "many_short": ("f16", 64, 2, 2, [3, 1, 2, 5] * 40, [4, 1, 70, 33] * 40, {}),
 }
 
@@ -97,9 +109,10 @@ def test_bits_behind_the_last_node_are_ignored():
 
 @pytest.mark.parametrize("kv", ["f16", "bf16", "e4m3"])
 @pytest.mark.parametrize("ctx", [12, 60, 1500])
-def test_masked_rows_may_hold_anything(kv, ctx):
+@pytest.mark.parametrize("group", [1, 4])
+def test_masked_rows_may_hold_anything(kv, ctx, group):
     """Keys and values of nodes that a node does not see are infinite or NaN: its row does not change."""
-    c = TreeCase(kv, 128, 2, 4, [12], [ctx], seed=5)
+    c = TreeCase(kv, 128, 2, group, [12], [ctx], seed=5)
     before = c.to_device().run().clone()
     bad = 7  # the node that holds them: whoever sees it gives NaN, the others what they gave
     at = ctx - 12 + bad
@@ -114,8 +127,9 @@ def test_masked_rows_may_hold_anything(kv, ctx):
     assert torch.isnan(got[:12][sees.cuda()]).all()
 
 
-def test_infinite_values_reach_the_nodes_that_see_them():
-    c = TreeCase("f16", 128, 1, 4, [6], [300], seed=6).to_device()
+@pytest.mark.parametrize("group", [2, 4])
+def test_infinite_values_reach_the_nodes_that_see_them(group):
+    c = TreeCase("f16", 128, 1, group, [6], [300], seed=6).to_device()
     before = c.run().clone()
     at = 300 - 6 + 3
     c.v_cache[int(c.bt_host[0, at // 16]), 0, at % 16, 5] = float("inf")
@@ -161,9 +175,10 @@ def test_strided_rows():
     assert torch.all(out[..., 128:] == 77.0)
 
 
-@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
-def test_placement_and_repetition_change_nothing(kv):
-    args = (kv, 128, 2, 4, [9, 33, 1], [100, 2222, 640])
+@pytest.mark.parametrize("kv", ["f16", "bf16", "e4m3"])
+@pytest.mark.parametrize("counts", [[9, 33, 1], [4, 1, 3]])
+def test_placement_and_repetition_change_nothing(kv, counts):
+    args = (kv, 128, 2, 4, counts, [100, 2222, 640])
     a = TreeCase(*args, seed=10).to_device()
     first = a.run().clone()
     for fill in (0, 0x7f):
@@ -207,10 +222,21 @@ def test_other_stream_and_graph():
         check(d, c.out)
 
 
+@pytest.mark.parametrize("kv", ["f16", "bf16", "e4m3"])
+def test_many_runs_are_the_same(kv):
+    """A race between the kernels' roles shows as bits that differ from run to run: ragged parts, rings that wrap."""
+    for counts, lens in (([33, 64, 2, 17] * 4, [3000, 70, 999, 400] * 4), ([5, 9, 6], [60, 90, 200]), ([2, 4, 1] * 5, [4000, 40, 333] * 5)):
+        c = TreeCase(kv, 128, 4, 4, counts, lens, seed=15).to_device()
+        first = c.run().clone()
+        for _ in range(40):
+            assert torch.equal(c.run(out=torch.full_like(c.out, 77.0)), first)
+
+
 @pytest.mark.parametrize("kv", ["f16", "e4m3"])
-def test_out_of_contract_sequences_are_left_alone(kv):
+@pytest.mark.parametrize("group", [1, 4])
+def test_out_of_contract_sequences_are_left_alone(kv, group):
     """A sequence the device finds out of contract sets its bit; the others are computed."""
-    c = TreeCase(kv, 128, 2, 4, [5, 9, 6], [60, 90, 200], seed=14).to_device()
+    c = TreeCase(kv, 128, 2, group, [5, 9, 6], [60, 90, 200], seed=14).to_device()
     good = c.run().clone()
     word = torch.zeros(1, dtype=torch.int32, device="cuda")
 
