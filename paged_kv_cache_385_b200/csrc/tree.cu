@@ -12,7 +12,7 @@
 // memory, two S buffers in tensor memory), softmax by 4 warps with a row per thread, P over S in tensor
 // memory, O += P V (A from tensor memory). Warps: 0-3 softmax, Q loads and epilogue; 4 TMA producer of K;
 // 5 QK issuer and owner of the tensor memory; 6 TMA producer of V; 7 PV issuer. e4m3 pages land as they
-// are (warp 4 brings both) and two pairs of warps widen them into the f16 operand tiles (8-9 K, 6 and 10 V).
+// are (warp 4 brings both) and two pairs of warps widen them into the f16 operand tiles (8-9 K, 10-11 V).
 // Two CTAs per SM.
 #include <algorithm>
 #include <type_traits>
@@ -27,9 +27,8 @@ namespace {
 
 constexpr int kRows = kTreeRows;  // query rows of an item
 constexpr int kKeys = 64;   // keys of a block
-using Pol = tree::Policy<kKeys, kRows, 8, 4, 6>;  // units are blocks
+using Pol = tree::Policy<kKeys, kRows, 10, 4, 4>;  // units are blocks
 using tree::Part;
-using tree::visible_bits;
 constexpr int kParts = 4;  // parts handed on and not yet left by every role
 constexpr uint32_t kQHalf = kRows * 128;  // a 64-element (128-byte) column half of the Q tile
 constexpr uint32_t kHalf = kKeys * 128;   // of a K or V tile
@@ -57,9 +56,9 @@ struct Layout {
   static constexpr uint32_t kRawVOff = kRawKOff + kRawStages * kRawTile;
   static constexpr uint32_t kBarOff = kRawVOff + kRawStages * kRawTile;
   static constexpr uint32_t kSmemBytes = kBarOff + kBarBytes;
-  static constexpr int kThreads = kFp8 ? 352 : 256;
+  static constexpr int kThreads = kFp8 ? 384 : 256;
   // Scores of a row that its thread holds at a time: all 64 of a block, or, where registers do not
-  // suffice (704 threads an SM, or the cap's arithmetic), 32 that are read twice from tensor memory.
+  // suffice (768 threads an SM, or the cap's arithmetic), 32 that are read twice from tensor memory.
   static constexpr int kHeld = kFp8 || kCap ? 32 : 64;
   // P is 2^(s - m + kShift): f16 keeps 7 more binades of small weights before it rounds them away
   // (2^(8 + 7) is still finite); bf16 has float32's range.
@@ -147,20 +146,8 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
   }
   const uint32_t bar = base + L::kBarOff;
   auto B = [&](int i) { return bar + 8u * i; };
-  pdl_wait();
 
-  // ---- this CTA's span ------------------------------------------------------------------------------
-  tree::Cursor<Pol> cur;
-  {
-    int64_t* before = reinterpret_cast<int64_t*>(smem);  // in the ring before it is used
-    tree::sum_costs<Pol, L::kThreads>(p, before);
-    if (!cur.start<L::kThreads>(p, before, blockIdx.x, gridDim.x)) {
-      if (threadIdx.x == 0) tree::describe_none(p, blockIdx.x);
-      return;
-    }
-  }
-  __syncthreads();  // the shares are read: the ring may be written
-
+  // ---- barriers and tensor memory, then this CTA's span --------------------------------------------
   if (threadIdx.x == 0) {
     mbar_init(B(kQFull), 4);
     for (int i = 0; i < L::kKStages; ++i) {
@@ -195,7 +182,12 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
   }
   if (warp == 5) tc05::alloc(B(kTmemSlot), kTmemCols);
   tc05::fence_before_sync();
-  __syncthreads();
+  pdl_wait();  // nothing that the kernel before may have written is read above
+  tree::Cursor<Pol> cur;
+  int64_t* before = reinterpret_cast<int64_t*>(smem);  // in the ring before it is used
+  tree::sum_costs<Pol, L::kThreads>(p, before);
+  cur.start<L::kThreads>(p, before, blockIdx.x, gridDim.x);  // (an empty span: the roles find no part)
+  __syncthreads();  // the shares are read: the ring may be written
   tc05::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kBarOff + 8 * kTmemSlot);
   const uint32_t tS0 = tmem, tO = tmem + 2 * kKeys;
@@ -316,10 +308,10 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     if (!ok && lane == 0) atomicOr(p.err, 4u);
   };
 
-  if (L::kFp8 && (warp >= 8 || warp == 6)) {
+  if (L::kFp8 && warp >= 8) {
     if constexpr (L::kFp8) {
-      if (warp == 8 || warp == 9) widen_all(warp - 8, L::kRawKOff, kRawKFull0, kRawKEmpty0, L::kKOff, L::kKStages, kKFull0, kKEmpty0);
-      else widen_all(warp == 10, L::kRawVOff, kRawVFull0, kRawVEmpty0, L::kVOff, L::kVStages, kVFull0, kVEmpty0);
+      if (warp < 10) widen_all(warp - 8, L::kRawKOff, kRawKFull0, kRawKEmpty0, L::kKOff, L::kKStages, kKFull0, kKEmpty0);
+      else widen_all(warp - 10, L::kRawVOff, kRawVFull0, kRawVEmpty0, L::kVOff, L::kVStages, kVFull0, kVEmpty0);
     }
   } else if (warp == 4) {
     // ---- TMA producer of K (e4m3: of both), and the schedule -----------------------------------------
@@ -346,7 +338,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     }
   } else if (warp == 6) {
     // ---- TMA producer of V ---------------------------------------------------------------------------
-    if (lane == 0) {
+    if (lane == 0 && !L::kFp8) {
       prefetch_tensormap(&vmap);
       for (int it = 0, g = 0; ok; ++it) {
         const uint64_t deadline = globaltimer_ns() + kWaitNs;
@@ -438,7 +430,8 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     const uint32_t inv_g = (65536u + G - 1) / G;
     // A negative scale turns Q's sign (load_q), so that the largest product gives the largest score.
     const bool negate = p.score_scale < 0.f;
-    const float sl2 = fabsf(p.score_scale) * 1.4426950408889634f;
+    // (A scale of 0 becomes one that makes every finite score 0 and leaves a masked score's -inf.)
+    const float sl2 = fmaxf(fabsf(p.score_scale) * 1.4426950408889634f, 1e-37f);
     // Capped scores: cap * tanh(s / cap) = cap - 2 cap / (1 + 2^(u s)), in log2 units.
     const float cap2 = kCap ? p.softcap * 1.4426950408889634f : 0.f;
     const float cap_u = kCap ? 2.f * sl2 / p.softcap : 0.f;
@@ -549,23 +542,14 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         if (threadIdx.x < 8) bad_nodes[threadIdx.x] = 0u;
         ok = ok && meet(deadline);
         if (!ok) break;
-        if (p.mask && valid) {
-          const uint64_t* words = p.mask + static_cast<int64_t>(P->q0 + node) * p.mask_words;
-          asm volatile("prefetch.global.L1 [%0];" ::"l"(words));
-        }
       }
       // m: the reference P and l are taken against (lazily raised); past the last row, P is 0 against it.
       float m = valid ? -INFINITY : INFINITY, l = 0.f;
       // Block j's P from its S. kMasked: some row may not see all of its keys.
-      auto softmax = [&](auto masked_tag, int j) -> bool {
+      auto softmax = [&](auto masked_tag, int j, uint64_t vis) -> bool {
         constexpr bool kMasked = decltype(masked_tag)::value;
         const int gb = g + j - j0;
         const uint32_t tS = tS0 + (gb & 1) * kKeys + lane_off;
-        uint64_t vis = ~0ull;
-        if constexpr (kMasked) {
-          vis = valid ? visible_bits(p, P, node, j * kKeys) : 0ull;
-          __syncwarp();
-        }
         // The block's largest score in log2 units: cap and scale are monotone, so they are applied to the
         // largest raw score alone.
         float sv[L::kHeld], top = -INFINITY;
@@ -602,7 +586,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             weights(x[2 * k], x[2 * k + 1], nref);
-            if constexpr (kMasked) {
+            if constexpr (kMasked && (kCap || L::kHeld == 32)) {  // (else the score is -inf already)
               if (!(bits >> (2 * k) & 1u)) x[2 * k] = 0.f;
               if (!(bits >> (2 * k + 1) & 1u)) x[2 * k + 1] = 0.f;
             }
@@ -648,15 +632,30 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
       for (const int whole_end = min(j_mask, j1 - 1); j < whole_end; ++j) {
         const int gb = g + j - j0;
         ok = got_s(gb);
-        if (!ok || (working && !softmax(std::false_type{}, j))) {
+        if (!ok || (working && !softmax(std::false_type{}, j, ~0ull))) {
           ok = false;
           break;
         }
         give_p(gb);
       }
+      // Words of the row's mask are loaded two blocks before they are needed: a block's are w and w + 1.
+      int w = (j * kKeys - P->start) >> 6;
+      uint64_t lo = 0ull, hi = 0ull, ahead = 0ull;
+      if (valid) {
+        lo = tree::mask_word(p, P, node, w);
+        hi = tree::mask_word(p, P, node, w + 1);
+        ahead = tree::mask_word(p, P, node, w + 2);
+      }
+      __syncwarp();
 #pragma unroll 1
       for (; ok && j < j1; ++j) {
         const int gb = g + j - j0;
+        const uint64_t vis = valid ? tree::visible_bits(lo, hi, P->start, P->ctx, j * kKeys) : 0ull;
+        ++w;
+        lo = hi;
+        hi = ahead;
+        if (valid) ahead = tree::mask_word(p, P, node, w + 2);
+        __syncwarp();
         ok = got_s(gb);
         if (!ok) break;
         if (j == j1 - 1) {  // the part's last QK has run: the next part's Q starts on its way
@@ -664,8 +663,9 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
           ok = __all_sync(kFull, N != nullptr);
           if (!ok) break;
           if (N->j0 < N->j1) start_q(N);
+          __syncwarp();
         }
-        if (working && !softmax(std::true_type{}, j)) {
+        if (working && !softmax(std::true_type{}, j, vis)) {
           ok = false;
           break;
         }
@@ -673,33 +673,34 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         // holds infinities or NaN: rows behind the context are zeroed, and a node's non-finite elements
         // too, the node noted for the epilogue, which gives them to the rows that do see it.
         if (j >= j_mask) {
-          // With one V stage the barrier may still lie in block gb - 1's phase, whose predecessor has the
-          // parity waited for: P.V(gb - 1) must have run first. (With more, S(gb) says that P.V(gb - 2)
-          // has, so the stage's barrier lies in block gb's phase.)
-          bool landed = L::kVStages > 1 || gb == 0 ||
-                        mbar_wait_bounded(B(kODone0 + ((gb - 1) & 1)), ((gb - 1) >> 1) & 1, deadline);
+          // V's barrier must lie in block gb's phase (a wait on an older one's parity would return at once):
+          // it does once the product that emptied the stage has run. With two stages or more that is so
+          // already, since this warp has seen S(gb), whose QK followed P.V(gb - 2).
+          const int emptied = gb - L::kVStages;
+          bool landed = L::kVStages > 1 || emptied < 0 ||
+                        mbar_wait_bounded(B(kODone0 + (emptied & 1)), (emptied >> 1) & 1, deadline);
           landed = landed && mbar_wait_bounded(B(kVFull0 + gb % L::kVStages), (gb / L::kVStages) & 1, deadline);
           if (!__all_sync(kFull, landed)) {
             ok = false;
             break;
           }
           constexpr int C = D / 8;
-          constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u;
+          // An exponent of all ones carries into its half's sign place when its lowest bit is added.
+          constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u, kLow = kBf16 ? 0x00800080u : 0x04000400u;
           const uint32_t vb = base + L::kVOff + (gb % L::kVStages) * L::kTile;
           const int t0 = j * kKeys, start = P->start, first = max(start - t0, 0), held = P->ctx - t0;
-#pragma unroll 2
+#pragma unroll 4
           for (int x = threadIdx.x; x < (kKeys - first) * C; x += 128) {
             const int row = first + x / C, c = x % C;
             const uint32_t a = vb + (c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-            uint32_t w[4], odd = 0u;
+            uint32_t w[4];
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+            uint32_t odd = 0u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t is = row < held ? __vcmpeq2(w[i] & kExp, kExp) : 0xffffffffu;
-              odd |= is;
-              w[i] &= ~is;
-            }
-            if (odd) {
+            for (int i = 0; i < 4; ++i) odd |= (w[i] & kExp) + kLow;
+            if ((odd & 0x80008000u) || row >= held) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[i] = row < held ? w[i] & ~__vcmpeq2(w[i] & kExp, kExp) : 0u;
               if (row < held) {
                 const int nd = t0 + row - start;
                 atomicOr(const_cast<uint32_t*>(&bad_nodes[nd >> 5]), 1u << (nd & 31));
@@ -749,7 +750,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
 #pragma unroll 1
               for (uint32_t bits = bad_nodes[w]; bits; bits &= bits - 1) {
                 const int nd = 32 * w + __ffs(bits) - 1, t = P->start + nd;
-                if (!(visible_bits(p, P, node, t) & 1ull)) continue;
+                if (!(tree::mask_word(p, P, node, nd >> 6) >> (nd & 63) & 1ull)) continue;
                 const int64_t at = ((static_cast<int64_t>(bt[t >> 4]) * p.num_kv_heads + P->hk) * 16 + (t & 15)) * D + c * 32;
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {

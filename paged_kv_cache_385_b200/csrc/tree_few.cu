@@ -63,7 +63,7 @@ struct RowMath : TcMath<C, D, NT> {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int row = nt * 8 + 2 * q4 + j;
-        seen[nt][j] = row < P.rows ? static_cast<uint32_t>(tree::visible_bits(p, &P, row / G, P.start)) : 0u;
+        seen[nt][j] = row < P.rows ? static_cast<uint32_t>(tree::mask_word(p, &P, row / G, 0) & tree::low_ones(P.ctx - P.start)) : 0u;
       }
     }
   }

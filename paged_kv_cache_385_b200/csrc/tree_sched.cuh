@@ -105,6 +105,8 @@ struct Cursor {
     len = max((total + spans - 1) / spans, static_cast<int64_t>(Pol::kMinSpan));
     beg = len * span;
     end = min(beg + len, total);
+    at = end;
+    s = p.num_seqs;
     if (beg >= total) return false;
     int lo = 0, hi = T - 1;  // the last share that starts at or before the span
     while (lo < hi) {
@@ -169,24 +171,18 @@ struct Cursor {
 
 __device__ __forceinline__ uint64_t low_ones(int n) { return n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1); }
 
-// The keys t0 .. t0 + 63 that a node sees, as bits.
+// Word w of the nodes of its sequence that a node sees, as bits (0 outside the mask).
 template <class P>
-__device__ __forceinline__ uint64_t visible_bits(const TreeParams& p, const P* part, int node, int t0) {
-  uint64_t v;
-  if (!p.mask) {
-    v = low_ones(part->start + node + 1 - t0);
-  } else {
-    const uint64_t* row = p.mask + static_cast<int64_t>(part->q0 + node) * p.mask_words;
-    const int o = t0 - part->start;
-    if (o < 0) {
-      v = low_ones(-o) | (o > -64 ? row[0] << -o : 0ull);
-    } else {
-      const int w = o >> 6, sh = o & 63;
-      v = w < p.mask_words ? row[w] >> sh : 0ull;
-      if (sh && w + 1 < p.mask_words) v |= row[w + 1] << (64 - sh);
-    }
-  }
-  return v & low_ones(part->ctx - t0);
+__device__ __forceinline__ uint64_t mask_word(const TreeParams& p, const P* part, int node, int w) {
+  if (!p.mask) return low_ones(node + 1 - 64 * w);
+  if (w < 0 || w >= p.mask_words) return 0ull;
+  return p.mask[static_cast<int64_t>(part->q0 + node) * p.mask_words + w];
+}
+
+// The keys t0 .. t0 + 63 that a node sees, from words floor((t0 - start) / 64) and the next of its bits.
+__device__ __forceinline__ uint64_t visible_bits(uint64_t lo, uint64_t hi, int start, int ctx, int t0) {
+  const int o = t0 - start, sh = o & 63;  // bit sh of lo is key t0's
+  return ((sh ? lo >> sh | hi << (64 - sh) : lo) | low_ones(-o)) & low_ones(ctx - t0);
 }
 
 __device__ __forceinline__ float rcp_approx(float x) {
