@@ -1129,6 +1129,7 @@ int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache,
   p.softcap = softcap;
   p.v_scale = v_scale;
   const pa::TreePlan plan = pa::tree_plan(B, num_kv_heads, p.group, max_query_len, max_ctx);
+  p.tile_rows = plan.rows;
   p.spans = plan.spans;
   size_t ml_off = 0, desc_off = 0;
   if (const size_t need = tree_workspace(D, plan, &ml_off, &desc_off)) {

@@ -197,7 +197,8 @@ struct TreeParams {
   float score_scale;  // scale * k_scale
   float softcap;      // 0 = none
   float v_scale;
-  int32_t spans;  // workers (CTAs or warps), each with an equal span of the batch's keys
+  int32_t tile_rows;  // query rows of an item at most, and
+  int32_t spans;      // workers (CTAs or warps), each with an equal span of the batch's keys (TreePlan's)
   // Rows of items that spans cut; all null when no context can be cut. Span c owns slots 2 c (its first
   // item, begun in an earlier span) and 2 c + 1 (its last, ended in a later one).
   float* ws_acc;     // [2 spans][D / 4][rows of a tile][4]

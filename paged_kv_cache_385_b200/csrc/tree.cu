@@ -25,9 +25,11 @@
 namespace pa {
 namespace {
 
-constexpr int kRows = kTreeRows;  // query rows of an item
-constexpr int kKeys = 64;   // keys of a block
-using Pol = tree::Policy<kKeys, kRows, 10, 4, 4>;  // units are blocks
+constexpr int kRows = kTreeRows;  // query rows of a tile
+constexpr int kKeys = 64;         // keys of a block
+// The schedule of items of NT tiles; its units are blocks.
+template <int NT>
+using Pol = tree::Policy<kKeys, NT * kRows, 10, 4, 4>;
 using tree::Part;
 constexpr int kParts = 4;  // parts handed on and not yet left by every role
 constexpr uint32_t kQHalf = kRows * 128;  // a 64-element (128-byte) column half of the Q tile
@@ -36,57 +38,61 @@ constexpr uint32_t kHalf = kKeys * 128;   // of a K or V tile
 // sum keep the older reference, and P stays below 2^8.
 constexpr float kLazyRescale = 8.f;
 
-constexpr uint32_t kBarBytes = 640;  // barriers and what the roles hand each other
+constexpr uint32_t kBarBytes = 896;  // barriers and what the roles hand each other
 
-template <KvType KV, int D, bool kCap>
+template <KvType KV, int D, bool kCap, int NT>
 struct Layout {
   static constexpr bool kBf16 = KV == KvType::BF16;  // operand type (e4m3 pages are widened to f16)
   static constexpr bool kFp8 = KV == KvType::E4M3;
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kQTile = kHalves * kQHalf;
   static constexpr uint32_t kTile = kHalves * kHalf;
-  static constexpr int kKStages = kFp8 ? 1 : (D == 128 ? 3 : 4), kVStages = kFp8 ? 1 : (D == 128 ? 2 : 4);
+  static constexpr int kKStages = NT == 2 ? (kFp8 ? 2 : (D == 128 ? 5 : 8)) : (kFp8 ? 1 : (D == 128 ? 3 : 4));
+  static constexpr int kVStages = NT == 2 ? kKStages : (kFp8 ? 1 : (D == 128 ? 2 : 4));
   // e4m3: pages land in rings of their own and are widened into the operand tiles.
   static constexpr uint32_t kRawTile = kFp8 ? kHalf : 0;
-  static constexpr int kRawStages = 3;
+  static constexpr int kRawStages = NT == 2 ? 6 : 3;
   static constexpr uint32_t kQOff = 0;
-  static constexpr uint32_t kKOff = kQTile;
+  static constexpr uint32_t kKOff = NT * kQTile;
   static constexpr uint32_t kVOff = kKOff + kKStages * kTile;
   static constexpr uint32_t kRawKOff = kVOff + kVStages * kTile;
   static constexpr uint32_t kRawVOff = kRawKOff + kRawStages * kRawTile;
   static constexpr uint32_t kBarOff = kRawVOff + kRawStages * kRawTile;
   static constexpr uint32_t kSmemBytes = kBarOff + kBarBytes;
-  static constexpr int kThreads = kFp8 ? 384 : 256;
+  static_assert(kSmemBytes <= (NT == 2 ? 232448 : 115712), "shared memory of one or two CTAs to an SM");
+  static constexpr int kSoftWarps = 4 * NT;  // the roles' warps follow them: K producer, QK issuer, V producer,
+                                             // PV issuer, and with e4m3 four that widen
+  static constexpr int kThreads = 32 * (kSoftWarps + (kFp8 ? 8 : 4));
   // Scores of a row that its thread holds at a time: all 64 of a block, or, where registers do not
   // suffice (768 threads an SM, or the cap's arithmetic), 32 that are read twice from tensor memory.
-  static constexpr int kHeld = kFp8 || kCap ? 32 : 64;
+  static constexpr int kHeld = (kFp8 && NT == 1) || kCap ? 32 : 64;
   // P is 2^(s - m + kShift): f16 keeps 7 more binades of small weights before it rounds them away
   // (2^(8 + 7) is still finite); bf16 has float32's range.
   static constexpr float kShift = kBf16 ? 0.f : 7.f;
 };
-constexpr uint32_t kTmemCols = 256;  // two S buffers of kKeys columns, then O's D columns
+constexpr uint32_t kTmemCols = 256;  // of a tile: two S buffers of kKeys columns, then O's D columns
 
 enum {
-  kQFull = 0,    // 4 softmax warps: the item's Q tile is in place
-  kKFull0 = 1,   // up to 4
-  kKEmpty0 = 5,  // up to 4
-  kVFull0 = 9,
-  kVEmpty0 = 13,
-  kSFull0 = 17,  // 2
-  kPFull0 = 19,  // 2: block gb arrives on kPFull0 + (gb & 1)
-  kODone0 = 21,  // 2: P(gb).V commits to kODone0 + (gb & 1)
-  kAllDone = 23,
-  kOFree = 24,   // the epilogue has read O (4 softmax warps)
-  kMeet = 25,    // the softmax warps meet (4)
-  kTmemSlot = 26,
-  kBadNodes = 27,  // 256 bits: nodes whose V row holds infinities or NaN
-  kRawKFull0 = 31,  // 3 each: e4m3 pages landed, and widened (2 warps)
-  kRawKEmpty0 = 34,
-  kRawVFull0 = 37,
-  kRawVEmpty0 = 40,
-  kPartFull0 = 43,   // kParts: a part is written (the K producer)
-  kPartEmpty0 = 47,  // kParts: every role has left it
-  kPart0 = 52,       // kParts parts
+  kQFull = 0,    // the softmax warps: the item's Q tiles are in place
+  kKFull0 = 1,   // up to 8
+  kKEmpty0 = 9,
+  kVFull0 = 17,
+  kVEmpty0 = 25,
+  kSFull0 = 33,  // tile t's block gb: + 2 t + (gb & 1), as for the next two
+  kPFull0 = 37,
+  kODone0 = 41,  // P(gb).V has run
+  kAllDone = 45,
+  kOFree = 46,   // the epilogue has read O (the softmax warps)
+  kMeet = 47,    // the softmax warps meet
+  kTmemSlot = 48,
+  kBadNodes = 49,  // 256 bits: nodes whose V row holds infinities or NaN
+  kRawKFull0 = 53,  // up to 6 each: e4m3 pages landed, and widened (2 warps)
+  kRawKEmpty0 = 59,
+  kRawVFull0 = 65,
+  kRawVEmpty0 = 71,
+  kPartFull0 = 77,   // kParts: a part is written (the K producer)
+  kPartEmpty0 = 81,  // kParts: every role has left it
+  kPart0 = 86,       // kParts parts
 };
 static_assert(kPartFull0 + kParts <= kPartEmpty0 && kPartEmpty0 + kParts <= kPart0, "barrier slots");
 static_assert(sizeof(Part) == 48 && 8 * kPart0 % 16 == 0 && 8 * kPart0 + kParts * sizeof(Part) <= kBarBytes, "barrier area");
@@ -132,11 +138,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // R / G for R < 4096 and G <= 16, by a multiplication: inv_g = ceil(65536 / G).
 __device__ __forceinline__ int div_group(int R, uint32_t inv_g) { return static_cast<int>((R * inv_g) >> 16); }
 
-template <KvType KV, bool kQBf16, int D, bool kCap>
-__global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
+template <KvType KV, bool kQBf16, int D, bool kCap, int NT>
+__global__ void __launch_bounds__(Layout<KV, D, kCap, NT>::kThreads, NT == 2 ? 1 : 2)
     tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const TreeParams p) {
-  using L = Layout<KV, D, kCap>;
+  using L = Layout<KV, D, kCap, NT>;
   constexpr bool kBf16 = L::kBf16;
+  constexpr int kSoft = L::kSoftWarps, kItemRows = NT * kRows;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -149,7 +156,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
 
   // ---- barriers and tensor memory, then this CTA's span --------------------------------------------
   if (threadIdx.x == 0) {
-    mbar_init(B(kQFull), 4);
+    mbar_init(B(kQFull), kSoft);
     for (int i = 0; i < L::kKStages; ++i) {
       mbar_init(B(kKFull0 + i), L::kFp8 ? 2 : 1);
       mbar_init(B(kKEmpty0 + i), 1);
@@ -166,31 +173,30 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         mbar_init(B(kRawVEmpty0 + i), 2);
       }
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * NT; ++i) {
       mbar_init(B(kSFull0 + i), 1);
       mbar_init(B(kPFull0 + i), 4);
       mbar_init(B(kODone0 + i), 1);
     }
     for (int i = 0; i < kParts; ++i) {
       mbar_init(B(kPartFull0 + i), 1);
-      mbar_init(B(kPartEmpty0 + i), L::kFp8 ? 10 : 7);  // issuers, 4 softmax warps; V producer or 4 widening warps
+      mbar_init(B(kPartEmpty0 + i), kSoft + (L::kFp8 ? 6 : 3));  // issuers; V producer or 4 widening warps
     }
-    mbar_init(B(kOFree), 4);
-    mbar_init(B(kMeet), 4);
+    mbar_init(B(kOFree), kSoft);
+    mbar_init(B(kMeet), kSoft);
     mbar_init(B(kAllDone), 1);
     fence_barrier_init();
   }
-  if (warp == 5) tc05::alloc(B(kTmemSlot), kTmemCols);
-  tc05::fence_before_sync();
   pdl_wait();  // nothing that the kernel before may have written is read above
-  tree::Cursor<Pol> cur;
+  if (warp == kSoft + 1) tc05::alloc(B(kTmemSlot), NT * kTmemCols);
+  tc05::fence_before_sync();
+  tree::Cursor<Pol<NT>> cur;
   int64_t* before = reinterpret_cast<int64_t*>(smem);  // in the ring before it is used
-  tree::sum_costs<Pol, L::kThreads>(p, before);
-  cur.start<L::kThreads>(p, before, blockIdx.x, gridDim.x);  // (an empty span: the roles find no part)
+  tree::sum_costs<Pol<NT>, L::kThreads>(p, before);
+  cur.template start<L::kThreads>(p, before, blockIdx.x, gridDim.x);  // (an empty span: the roles find no part)
   __syncthreads();  // the shares are read: the ring may be written
   tc05::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kBarOff + 8 * kTmemSlot);
-  const uint32_t tS0 = tmem, tO = tmem + 2 * kKeys;
   bool ok = true;
   int issued_k = 0, issued_v = 0;  // producer lanes: fills issued (for the drain after a failure)
   constexpr uint64_t kWaitNs = 2000000000ull;
@@ -308,12 +314,13 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     if (!ok && lane == 0) atomicOr(p.err, 4u);
   };
 
-  if (L::kFp8 && warp >= 8) {
+  if (L::kFp8 && warp >= kSoft + 4) {
     if constexpr (L::kFp8) {
-      if (warp < 10) widen_all(warp - 8, L::kRawKOff, kRawKFull0, kRawKEmpty0, L::kKOff, L::kKStages, kKFull0, kKEmpty0);
-      else widen_all(warp - 10, L::kRawVOff, kRawVFull0, kRawVEmpty0, L::kVOff, L::kVStages, kVFull0, kVEmpty0);
+      const int w = warp - kSoft - 4;
+      if (w < 2) widen_all(w, L::kRawKOff, kRawKFull0, kRawKEmpty0, L::kKOff, L::kKStages, kKFull0, kKEmpty0);
+      else widen_all(w - 2, L::kRawVOff, kRawVFull0, kRawVEmpty0, L::kVOff, L::kVStages, kVFull0, kVEmpty0);
     }
-  } else if (warp == 4) {
+  } else if (warp == kSoft) {
     // ---- TMA producer of K (e4m3: of both), and the schedule -----------------------------------------
     if (lane == 0) {
       prefetch_tensormap(&kmap);
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
       }
       if (!ok) atomicOr(p.err, 4u);
     }
-  } else if (warp == 6) {
+  } else if (warp == kSoft + 2) {
     // ---- TMA producer of V ---------------------------------------------------------------------------
     if (lane == 0 && !L::kFp8) {
       prefetch_tensormap(&vmap);
@@ -351,8 +358,8 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
       }
       if (!ok) atomicOr(p.err, 4u);
     }
-  } else if (warp == 5) {
-    // ---- QK issuer: S(g) = Q K(g)^T into S buffer g & 1 ----------------------------------------------
+  } else if (warp == kSoft + 1) {
+    // ---- QK issuer: S(g) = Q K(g)^T into S buffer g & 1 of each tile ------------------------------------
     if (lane == 0) {
       constexpr uint32_t idesc = tc05::idesc_f16(kBf16, kRows, kKeys, false, false);
       for (int it = 0, g = 0; ok; ++it) {
@@ -360,34 +367,41 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         const volatile Part* P = take_part(it, deadline);
         ok = P != nullptr;
         if (!ok) break;
-        const int blocks = P->j1 - P->j0;
+        const int blocks = P->j1 - P->j0, rows = P->rows - P->tile * kItemRows;
         leave_part(it);
         if (blocks == 0) break;
         ok = mbar_wait_bounded(B(kQFull), it & 1, deadline);
         for (int j = 0; j < blocks && ok; ++j, ++g) {
-          // Buffer g & 1 holds P(g - 2) until P(g - 2).V has run. O_done is two barriers by parity: the
-          // one waited for here next completes for P(g).V, which needs the S issued below.
           const int st = g % L::kKStages;
-          if ((g >= 2 && !mbar_wait_bounded_poll(B(kODone0 + (g & 1)), ((g - 2) >> 1) & 1, deadline)) ||
-              !mbar_wait_bounded_poll(B(kKFull0 + st), (g / L::kKStages) & 1, deadline)) {
-            ok = false;
-            break;
-          }
-          tc05::fence_after_sync();
+          ok = mbar_wait_bounded_poll(B(kKFull0 + st), (g / L::kKStages) & 1, deadline);
           const uint32_t kb = base + L::kKOff + st * L::kTile;
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t cb = (ks & 3) * 32;
-            tc05::mma_f16(tS0 + (g & 1) * kKeys, tc05::smem_desc_sw128(base + L::kQOff + (ks >> 2) * kQHalf + cb, 16, 1024),
-                          tc05::smem_desc_sw128(kb + (ks >> 2) * kHalf + cb, 16, 1024), idesc, ks > 0);
+          for (int t = 0; t < NT; ++t) {
+            // Buffer g & 1 holds P(g - 2) until P(g - 2).V has run. O_done is two barriers by parity: the
+            // one waited for here next completes for P(g).V, which needs the S issued below.
+            const int buf = 2 * t + (g & 1);
+            if (!ok || (g >= 2 && !mbar_wait_bounded_poll(B(kODone0 + buf), ((g - 2) >> 1) & 1, deadline))) {
+              ok = false;
+              break;
+            }
+            tc05::fence_after_sync();
+            if (t == 0 || rows > t * kRows) {  // (a tile without rows only keeps step)
+              const uint32_t qb = base + L::kQOff + t * L::kQTile;
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t cb = (ks & 3) * 32;
+                tc05::mma_f16(tmem + t * kTmemCols + (g & 1) * kKeys, tc05::smem_desc_sw128(qb + (ks >> 2) * kQHalf + cb, 16, 1024),
+                              tc05::smem_desc_sw128(kb + (ks >> 2) * kHalf + cb, 16, 1024), idesc, ks > 0);
+              }
+            }
+            tc05::commit(B(kSFull0 + buf));
           }
-          tc05::commit(B(kSFull0 + (g & 1)));
-          tc05::commit(B(kKEmpty0 + st));
+          if (ok) tc05::commit(B(kKEmpty0 + st));
         }
       }
       if (!ok) atomicOr(p.err, 4u);
     }
-  } else if (warp == 7) {
+  } else if (warp == kSoft + 3) {
     // ---- PV issuer: O += P(g) V(g) ---------------------------------------------------------------------
     if (lane == 0) {
       constexpr uint32_t idesc = tc05::idesc_f16(kBf16, kRows, D, false, true);
@@ -396,26 +410,36 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         const volatile Part* P = take_part(it, deadline);
         ok = P != nullptr;
         if (!ok) break;
-        const int blocks = P->j1 - P->j0;
+        const int blocks = P->j1 - P->j0, rows = P->rows - P->tile * kItemRows;
+        const int tail = P->start / kKeys - P->j0;  // from this block on the softmax warps clear rows of V
         leave_part(it);
         if (blocks == 0) break;
         // The part's first product overwrites O: the epilogue before it must have read it.
         if (it > 0) ok = mbar_wait_bounded(B(kOFree), (it - 1) & 1, deadline);
         for (int j = 0; j < blocks && ok; ++j, ++g) {
           const int st = g % L::kVStages;
-          if (!mbar_wait_bounded_poll(B(kPFull0 + (g & 1)), (g >> 1) & 1, deadline) ||
-              !mbar_wait_bounded_poll(B(kVFull0 + st), (g / L::kVStages) & 1, deadline)) {
-            ok = false;
-            break;
-          }
-          tc05::fence_after_sync();
           const uint32_t vb = base + L::kVOff + st * L::kTile;
 #pragma unroll
-          for (int kt = 0; kt < kKeys / 16; ++kt)
-            tc05::mma_f16_ts(tO, tS0 + (g & 1) * kKeys + kt * 8, tc05::smem_desc_sw128(vb + kt * 2048, kHalf, 1024), idesc,
-                             j > 0 || kt > 0);
-          tc05::commit(B(kODone0 + (g & 1)));
-          tc05::commit(B(kVEmpty0 + st));
+          for (int t = 0; t < NT; ++t) {
+            const int buf = 2 * t + (g & 1);
+            // (Every tile's warps share that work: all of them must have done theirs before the first product.)
+            if (!mbar_wait_bounded_poll(B(kPFull0 + buf), (g >> 1) & 1, deadline) ||
+                (NT == 2 && t == 0 && j >= tail && !mbar_wait_bounded_poll(B(kPFull0 + buf + 2), (g >> 1) & 1, deadline)) ||
+                (t == 0 && !mbar_wait_bounded_poll(B(kVFull0 + st), (g / L::kVStages) & 1, deadline))) {
+              ok = false;
+              break;
+            }
+            tc05::fence_after_sync();
+            if (t == 0 || rows > t * kRows) {
+              const uint32_t tt = tmem + t * kTmemCols;
+#pragma unroll
+              for (int kt = 0; kt < kKeys / 16; ++kt)
+                tc05::mma_f16_ts(tt + 2 * kKeys, tt + (g & 1) * kKeys + kt * 8, tc05::smem_desc_sw128(vb + kt * 2048, kHalf, 1024),
+                                 idesc, j > 0 || kt > 0);
+            }
+            tc05::commit(B(kODone0 + buf));
+          }
+          if (ok) tc05::commit(B(kVEmpty0 + st));
         }
       }
       // Every QK has completed before its softmax finished, so this covers all of the CTA's MMAs.
@@ -425,7 +449,10 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     }
   } else {
     // ---- softmax warps: thread = row -----------------------------------------------------------------
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    const int t = warp >> 2, quad = warp & 3;  // the tile, and the warp's 32 tensor-memory lanes of it
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS0 = tmem + t * kTmemCols + lane_off, tO = tS0 + 2 * kKeys;
+    const int s_full = kSFull0 + 2 * t, p_full = kPFull0 + 2 * t, o_done = kODone0 + 2 * t;
     const int G = p.group;
     const uint32_t inv_g = (65536u + G - 1) / G;
     // A negative scale turns Q's sign (load_q), so that the largest product gives the largest score.
@@ -436,7 +463,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     const float cap2 = kCap ? p.softcap * 1.4426950408889634f : 0.f;
     const float cap_u = kCap ? 2.f * sl2 / p.softcap : 0.f;
     volatile uint32_t* bad_nodes = reinterpret_cast<volatile uint32_t*>(smem + L::kBarOff + 8 * kBadNodes);
-    int meets = 0, turn = 0;
+    int meets = 0;
     if (threadIdx.x == 0) tree::describe_none(p, blockIdx.x);
 
     auto score = [&](float s) -> float {  // a raw product in log2 units
@@ -457,7 +484,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
       x0 = ex2(t.x);
       x1 = ex2(t.y);
     };
-    // The four warps meet (a bounded wait: a warp that gave up does not come).
+    // The softmax warps meet (a bounded wait: a warp that gave up does not come).
     auto meet = [&](uint64_t deadline) -> bool {
       __syncwarp();
       if (lane == 0) mbar_arrive(B(kMeet));
@@ -467,19 +494,23 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
     };
     // Few rows keep only some warps busy. Those of the second half of the CTAs, which share their SMs with
     // the first half's, are turned by half a tile, so that the two use different quarters of the SM.
-    auto turn_of = [&](int rows_left) { return rows_left <= kRows / 2 && blockIdx.x * 2 >= gridDim.x ? kRows / 2 : 0; };
+    auto turn_of = [&](int rows_left) {
+      return NT == 1 && rows_left <= kRows / 2 && blockIdx.x * 2 >= gridDim.x ? kRows / 2 : 0;
+    };
     // A part's Q rows into the swizzled tile, as asynchronous copies of 16-byte chunks, a row's by
     // neighbouring lanes; rows past the last are zero (each row's products are its own, but zeros cost
-    // the tensor cores less power, and these kernels run into the GPU's power limit). start_q may run once the QKs of the part before have (this warp has seen its last S), finish_q
-    // hands the tile to the QK issuer.
+    // the tensor cores less power, and these kernels run into the GPU's power limit). start_q may run once
+    // the QKs of the part before have (this warp has seen its last S), finish_q hands the tile to the QK
+    // issuer.
     constexpr int kRowChunks = D / 8;
     auto q_addr = [&](int x) -> uint32_t {
-      const int row = warp * 32 + x / kRowChunks, c = x % kRowChunks;
-      return base + L::kQOff + (c >> 3) * kQHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+      const int row = quad * 32 + x / kRowChunks, c = x % kRowChunks;
+      return base + L::kQOff + t * L::kQTile + (c >> 3) * kQHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4);
     };
     auto start_q = [&](const volatile Part* P) {
-      const int row0 = P->tile * kRows, left = min(P->rows - row0, kRows), head0 = P->hk * G, c = lane % kRowChunks;
-      const int from = (warp * 32 - turn_of(left)) & (kRows - 1);  // the warp's first row of the tile
+      const int row0 = P->tile * kItemRows + t * kRows, left = min(P->rows - row0, kRows);
+      const int head0 = P->hk * G, c = lane % kRowChunks;
+      const int from = (quad * 32 - turn_of(left)) & (kRows - 1);  // the warp's first row of the tile
       const uint16_t* q0 = static_cast<const uint16_t*>(p.q) + P->q0 * p.q_stride_t + c * 8;
 #pragma unroll 4
       for (int x = lane; x < 32 * kRowChunks; x += 32) {
@@ -529,12 +560,12 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         finish_q();
       }
       // The tile's rows lie on the tensor-memory lanes in order, from lane `turn` on.
-      const int rows_left = min(P->rows - P->tile * kRows, kRows);
-      turn = turn_of(rows_left);
+      const int row0 = P->tile * kItemRows + t * kRows, rows_left = min(P->rows - row0, kRows);
+      const int turn = turn_of(rows_left);
       const int r = (static_cast<int>(threadIdx.x) - turn) & (kRows - 1);
       const bool valid = r < rows_left;
-      const bool working = ((warp * 32 - turn) & (kRows - 1)) < rows_left;  // warps without a row only keep step
-      const int node = valid ? div_group(P->tile * kRows + r, inv_g) : 0;
+      const bool working = ((quad * 32 - turn) & (kRows - 1)) < rows_left;  // warps without a row only keep step
+      const int node = valid ? div_group(row0 + r, inv_g) : 0;
       const int j_mask = P->start / kKeys;  // the first block that holds a drafted node or the end
       const bool had_tail = j1 > j_mask;
       if (had_tail) {  // no warp reads the bits of the part before any more; they are cleared
@@ -549,7 +580,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
       auto softmax = [&](auto masked_tag, int j, uint64_t vis) -> bool {
         constexpr bool kMasked = decltype(masked_tag)::value;
         const int gb = g + j - j0;
-        const uint32_t tS = tS0 + (gb & 1) * kKeys + lane_off;
+        const uint32_t tS = tS0 + (gb & 1) * kKeys;
         // The block's largest score in log2 units: cap and scale are monotone, so they are applied to the
         // largest raw score alone.
         float sv[L::kHeld], top = -INFINITY;
@@ -600,24 +631,24 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         // O's rescale waits for the P.V before it. Its barrier next completes for P(gb + 1).V, which
         // needs this warp's P(gb + 1): never two phases ahead.
         if (raise && j > j0) {
-          const bool done = mbar_wait_bounded(B(kODone0 + ((gb - 1) & 1)), ((gb - 1) >> 1) & 1, deadline);
+          const bool done = mbar_wait_bounded(B(o_done + ((gb - 1) & 1)), ((gb - 1) >> 1) & 1, deadline);
           if (!__all_sync(kFull, done)) return false;
           tc05::fence_after_sync();
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float v[32];
-            tc05::ld32(tO + lane_off + c * 32, v);
+            tc05::ld32(tO + c * 32, v);
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] *= alpha;
-            tc05::st32(tO + lane_off + c * 32, v);
+            tc05::st32(tO + c * 32, v);
           }
         }
         tc05::st_wait();
         return true;
       };
       auto got_s = [&](int gb) -> bool {
-        const bool got = working ? mbar_wait_bounded_poll(B(kSFull0 + (gb & 1)), (gb >> 1) & 1, deadline)
-                                 : mbar_wait_bounded(B(kSFull0 + (gb & 1)), (gb >> 1) & 1, deadline);
+        const bool got = working ? mbar_wait_bounded_poll(B(s_full + (gb & 1)), (gb >> 1) & 1, deadline)
+                                 : mbar_wait_bounded(B(s_full + (gb & 1)), (gb >> 1) & 1, deadline);
         if (!__all_sync(kFull, got)) return false;
         tc05::fence_after_sync();
         return true;
@@ -625,7 +656,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
       auto give_p = [&](int gb) {
         tc05::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(B(kPFull0 + (gb & 1)));
+        if (lane == 0) mbar_arrive(B(p_full + (gb & 1)));
       };
       // The blocks that every row sees whole, but for the part's last: a short loop.
       int j = j0;
@@ -678,7 +709,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
           // already, since this warp has seen S(gb), whose QK followed P.V(gb - 2).
           const int emptied = gb - L::kVStages;
           bool landed = L::kVStages > 1 || emptied < 0 ||
-                        mbar_wait_bounded(B(kODone0 + (emptied & 1)), (emptied >> 1) & 1, deadline);
+                        mbar_wait_bounded(B(o_done + (emptied & 1)), (emptied >> 1) & 1, deadline);
           landed = landed && mbar_wait_bounded(B(kVFull0 + gb % L::kVStages), (gb / L::kVStages) & 1, deadline);
           if (!__all_sync(kFull, landed)) {
             ok = false;
@@ -690,7 +721,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
           const uint32_t vb = base + L::kVOff + (gb % L::kVStages) * L::kTile;
           const int t0 = j * kKeys, start = P->start, first = max(start - t0, 0), held = P->ctx - t0;
 #pragma unroll 4
-          for (int x = threadIdx.x; x < (kKeys - first) * C; x += 128) {
+          for (int x = threadIdx.x; x < (kKeys - first) * C; x += 32 * kSoft) {
             const int row = first + x / C, c = x % C;
             const uint32_t a = vb + (c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4);
             uint32_t w[4];
@@ -721,7 +752,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
         if (N->j0 < N->j1) finish_q();  // before the epilogue, which the next part's first QK overlaps
       }
       // ---- epilogue ------------------------------------------------------------------------------------
-      if (!__all_sync(kFull, mbar_wait_bounded(B(kODone0 + (gl & 1)), (gl >> 1) & 1, deadline)) ||
+      if (!__all_sync(kFull, mbar_wait_bounded(B(o_done + (gl & 1)), (gl >> 1) & 1, deadline)) ||
           (had_tail && !meet(deadline))) {
         ok = false;
         break;
@@ -731,7 +762,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
       const bool whole = first == P->last;
       const int slot = 2 * blockIdx.x + (first == static_cast<int>(blockIdx.x));
       const float inv = l == 0.f ? 0.f : p.v_scale / l;
-      const int head = P->hk * G + P->tile * kRows + r - node * G;
+      const int head = P->hk * G + row0 + r - node * G;
       uint16_t* dst = static_cast<uint16_t*>(p.out) + (P->q0 + node) * p.o_stride_t + head * p.o_stride_h;
       uint32_t any_bad = 0u;
       if (had_tail) {
@@ -742,16 +773,16 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           float v[32];
-          tc05::ld32(tO + lane_off + c * 32, v);
+          tc05::ld32(tO + c * 32, v);
           if (any_bad && valid) {  // non-finite values of nodes that this row sees
             const int32_t* bt = p.block_tables + static_cast<int64_t>(P->s) * p.bt_stride;
 #pragma unroll 1
             for (int w = 0; w < 8; ++w) {
 #pragma unroll 1
               for (uint32_t bits = bad_nodes[w]; bits; bits &= bits - 1) {
-                const int nd = 32 * w + __ffs(bits) - 1, t = P->start + nd;
+                const int nd = 32 * w + __ffs(bits) - 1, at_token = P->start + nd;
                 if (!(tree::mask_word(p, P, node, nd >> 6) >> (nd & 63) & 1ull)) continue;
-                const int64_t at = ((static_cast<int64_t>(bt[t >> 4]) * p.num_kv_heads + P->hk) * 16 + (t & 15)) * D + c * 32;
+                const int64_t at = ((static_cast<int64_t>(bt[at_token >> 4]) * p.num_kv_heads + P->hk) * 16 + (at_token & 15)) * D + c * 32;
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
                   if constexpr (L::kFp8) {
@@ -775,13 +806,13 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
               *reinterpret_cast<uint4*>(dst + c * 32 + 8 * q) = o;
             }
           } else if (valid) {
-            float4* ws = reinterpret_cast<float4*>(p.ws_acc) + tree::ws_at<kRows, D>(slot, 8 * c, r);
+            float4* ws = reinterpret_cast<float4*>(p.ws_acc) + tree::ws_at<kItemRows, D>(slot, 8 * c, t * kRows + r);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) ws[q * kRows] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            for (int q = 0; q < 8; ++q) ws[q * kItemRows] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
           }
           __syncwarp();  // the tensor-memory load above is the whole warp's
         }
-        if (valid && !whole) p.ws_ml[slot * kRows + r] = make_float2(m, l);
+        if (valid && !whole) p.ws_ml[slot * kItemRows + t * kRows + r] = make_float2(m, l);
       }
       if (threadIdx.x == 0 && !whole && first == static_cast<int>(blockIdx.x)) tree::describe(p, blockIdx.x, P);
       tc05::fence_before_sync();
@@ -797,11 +828,11 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
   pdl_launch_dependents();
   tc05::fence_before_sync();
   const int any_fail = __syncthreads_or(!ok);
-  if (warp == 5) {
+  if (warp == kSoft + 1) {
     tc05::fence_after_sync();
-    tc05::dealloc(tmem, kTmemCols);
+    tc05::dealloc(tmem, NT * kTmemCols);
   }
-  if (any_fail && (warp == 4 || warp == 6) && lane == 0) {
+  if (any_fail && (warp == kSoft || warp == kSoft + 2) && lane == 0) {
     // A wait gave up, so copies in flight may not have been consumed: give them a bounded chance to land
     // before the shared memory goes. Only the last fill of each stage can be outstanding.
     const uint64_t drain_deadline = globaltimer_ns() + 100000000ull;
@@ -812,20 +843,25 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap>::kThreads, 2)
   }
 }
 
-template <KvType KV, bool kQBf16, int D, bool kCap>
+template <KvType KV, bool kQBf16, int D, bool kCap, int NT>
 cudaError_t launch_t(const CUtensorMap& km, const CUtensorMap& vm, const TreeParams& p, cudaStream_t st) {
-  using L = Layout<KV, D, kCap>;
-  auto kern = tree_kernel<KV, kQBf16, D, kCap>;
+  using L = Layout<KV, D, kCap, NT>;
+  auto kern = tree_kernel<KV, kQBf16, D, kCap, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
   if (e != cudaSuccess) return e;
   e = tree::launch_dependent(kern, dim3(p.spans), L::kThreads, L::kSmemBytes, st, km, vm, p);
   if (e != cudaSuccess || !p.ws_desc) return e;
-  return tree::launch_dependent(tree::merge_kernel<kQBf16, D, kRows>, dim3(p.spans, kRows / 8), 128, 0, st, p);
+  return tree::launch_dependent(tree::merge_kernel<kQBf16, D, NT * kRows>, dim3(p.spans, NT * kRows / 8), 128, 0, st, p);
+}
+
+template <KvType KV, bool kQBf16, int D, int NT>
+cudaError_t launch_cap(const CUtensorMap& km, const CUtensorMap& vm, const TreeParams& p, cudaStream_t st) {
+  return p.softcap > 0.f ? launch_t<KV, kQBf16, D, true, NT>(km, vm, p, st) : launch_t<KV, kQBf16, D, false, NT>(km, vm, p, st);
 }
 
 template <KvType KV, bool kQBf16, int D>
-cudaError_t launch_cap(const CUtensorMap& km, const CUtensorMap& vm, const TreeParams& p, cudaStream_t st) {
-  return p.softcap > 0.f ? launch_t<KV, kQBf16, D, true>(km, vm, p, st) : launch_t<KV, kQBf16, D, false>(km, vm, p, st);
+cudaError_t launch_tiles(const CUtensorMap& km, const CUtensorMap& vm, const TreeParams& p, cudaStream_t st) {
+  return p.tile_rows == 2 * kRows ? launch_cap<KV, kQBf16, D, 2>(km, vm, p, st) : launch_cap<KV, kQBf16, D, 1>(km, vm, p, st);
 }
 
 }  // namespace
@@ -839,18 +875,21 @@ static bool few(int64_t max_query_len, int group) { return max_query_len * group
 
 TreePlan tree_plan(int64_t num_seqs, int num_kv_heads, int group, int max_query_len, int64_t max_context_len) {
   TreePlan plan;
-  plan.rows = few(max_query_len, group) ? kTreeFewRows : kRows;
-  if (plan.rows == kTreeFewRows) {
+  if (few(max_query_len, group)) {
+    plan.rows = kTreeFewRows;
     plan.spans = tree_few_spans(num_seqs, num_kv_heads, max_query_len * group, max_context_len);
     plan.splits = tree_few_splits(max_context_len);
     return plan;
   }
+  const int64_t rows = static_cast<int64_t>(max_query_len) * group;
+  plan.rows = rows > kRows ? 2 * kRows : kRows;
   // (Each factor is capped where more cannot matter, so that no product overflows.)
   const auto cap = [](int64_t x) { return std::min<int64_t>(x, 1 << 20); };
-  const int64_t items = cap(cap(num_seqs) * num_kv_heads) * cap((static_cast<int64_t>(max_query_len) * group + kRows - 1) / kRows);
-  const int64_t blocks = (max_context_len + kKeys - 1) / kKeys, cost = cap(items) * (blocks + Pol::kItemCost);
-  plan.spans = static_cast<int>(std::min<int64_t>(kTreeMaxSpans, std::max<int64_t>(1, (cost + Pol::kMinSpan - 1) / Pol::kMinSpan)));
-  plan.splits = blocks > Pol::kWhole;
+  const int64_t items = cap(cap(num_seqs) * num_kv_heads) * cap((rows + plan.rows - 1) / plan.rows);
+  const int64_t blocks = (max_context_len + kKeys - 1) / kKeys, cost = cap(items) * (blocks + Pol<1>::kItemCost);
+  const int64_t most = kTreeMaxSpans / (plan.rows / kRows);
+  plan.spans = static_cast<int>(std::min<int64_t>(most, std::max<int64_t>(1, (cost + Pol<1>::kMinSpan - 1) / Pol<1>::kMinSpan)));
+  plan.splits = blocks > Pol<1>::kWhole;
   return plan;
 }
 
@@ -858,10 +897,10 @@ cudaError_t launch_decode_tree(KvType kv, QType q, int head_dim, const CUtensorM
                                const TreeParams& p, cudaStream_t st) {
   if (few(p.max_query_len, p.group)) return launch_decode_tree_few(kv, q, head_dim, km, vm, p, st);
   if (kv == KvType::BF16)
-    return head_dim == 128 ? launch_cap<KvType::BF16, true, 128>(km, vm, p, st) : launch_cap<KvType::BF16, true, 64>(km, vm, p, st);
+    return head_dim == 128 ? launch_tiles<KvType::BF16, true, 128>(km, vm, p, st) : launch_tiles<KvType::BF16, true, 64>(km, vm, p, st);
   if (kv == KvType::F16)
-    return head_dim == 128 ? launch_cap<KvType::F16, false, 128>(km, vm, p, st) : launch_cap<KvType::F16, false, 64>(km, vm, p, st);
-  return q == QType::BF16 ? launch_cap<KvType::E4M3, true, 128>(km, vm, p, st) : launch_cap<KvType::E4M3, false, 128>(km, vm, p, st);
+    return head_dim == 128 ? launch_tiles<KvType::F16, false, 128>(km, vm, p, st) : launch_tiles<KvType::F16, false, 64>(km, vm, p, st);
+  return q == QType::BF16 ? launch_tiles<KvType::E4M3, true, 128>(km, vm, p, st) : launch_tiles<KvType::E4M3, false, 128>(km, vm, p, st);
 }
 
 }  // namespace pa
