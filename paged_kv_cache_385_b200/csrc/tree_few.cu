@@ -19,7 +19,7 @@
 namespace pa {
 namespace {
 
-using Pol = tree::Policy<16, kTreeFewRows, 8, 16, 16>;  // units are pages
+using Pol = tree::Policy<16, kTreeFewRows, 4, 8, 6>;  // units are pages
 using tree::Part;
 
 template <KvType KV, QType QT, int D, int NT, int OCC>
