@@ -237,8 +237,12 @@ def test_many_runs_are_the_same(kv):
 def test_out_of_contract_sequences_are_left_alone(kv, group):
     """A sequence the device finds out of contract sets its bit; the others are computed."""
     c = TreeCase(kv, 128, 2, group, [5, 9, 6], [60, 90, 200], seed=14).to_device()
-    good = c.run().clone()
+    want, weight = c.oracle()
+    bound = c.bound(want, weight)
     word = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def right(got, a, b):  # (where contexts are cut goes by the whole batch's lengths, so bits may differ)
+        return bool((np.abs(got[a:b].double().cpu().numpy() - want[a:b]) <= bound[a:b]).all())
 
     def rerun(**kw):
         word.zero_()
@@ -249,10 +253,10 @@ def test_out_of_contract_sequences_are_left_alone(kv, group):
         c.lens[0] = bad
         got = rerun()
         assert int(word) == pa.PA_DEVERR_CTX_RANGE, bad
-        assert torch.all(got[:5] == 77.0) and torch.equal(got[5:20], good[5:20])
+        assert torch.all(got[:5] == 77.0) and right(got, 5, 20)
         c.lens.copy_(lens)
     got = rerun(max_context_len=150)
-    assert int(word) == pa.PA_DEVERR_CTX_RANGE and torch.all(got[14:20] == 77.0) and torch.equal(got[:14], good[:14])
+    assert int(word) == pa.PA_DEVERR_CTX_RANGE and torch.all(got[14:20] == 77.0) and right(got, 0, 14)
     start = c.start.clone()
     for at, value in ((3, 10 ** 6), (0, -1), (3, 13)):  # rows outside q; a negative count
         c.start[at] = value
@@ -262,5 +266,5 @@ def test_out_of_contract_sequences_are_left_alone(kv, group):
     c.bt[1, 2] = c.num_blocks
     got = rerun()
     assert int(word) == pa.PA_DEVERR_BAD_BLOCK
-    assert torch.equal(got[:5], good[:5]) and torch.equal(got[14:20], good[14:20])
+    assert right(got, 0, 5) and right(got, 14, 20)
     assert pa.pa_read_device_error(clear=True) == 0
