@@ -78,6 +78,9 @@ class PaRopeOpts(ctypes.Structure):
                 ("v_scale", ctypes.c_float), ("error_word", ctypes.c_void_p)]
 
 
+_ROPE_OPTS = struct.Struct("@ifffP")  # PaRopeOpts's layout
+
+
 class PagedAttentionError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str):
         super().__init__(f"{where}: {status_string(status)} ({status}): {detail}")
@@ -103,7 +106,7 @@ def _load() -> ctypes.CDLL:
         "pa_rope_opts_init": (None, [ctypes.POINTER(PaRopeOpts)]),
         "pa_rope_inv_freq": (ctypes.c_int, [ctypes.POINTER(F32), I32, ctypes.c_double, I32, ctypes.c_double, I64,
                                             ctypes.c_double, ctypes.c_double]),
-        "pa_rope_and_cache": (ctypes.c_int, [VP] * 9 + [ctypes.POINTER(PaRopeOpts), VP]),
+        "pa_rope_and_cache": (ctypes.c_int, [VP] * 11),
         "pa_decode_tree": (ctypes.c_int, [VP] * 8 + [I32, F32, F32, I32, ctypes.POINTER(PaDecodeOpts), VP]),
         "pa_decode_tree_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32]),
         "pa_commit_tree": (ctypes.c_int, [VP] * 10),
@@ -345,13 +348,10 @@ def pa_rope_and_cache(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], 
                       k_scale: float = 1.0, v_scale: float = 1.0, error_word: Optional[torch.Tensor] = None,
                       stream=None) -> None:
     """Rotate new tokens' queries and keys and write keys and values into their slots (see include/pa.h)."""
-    o = PaRopeOpts()
-    _lib.pa_rope_opts_init(ctypes.byref(o))
-    o.interleaved, o.magnitude, o.k_scale, o.v_scale = int(bool(interleaved)), magnitude, k_scale, v_scale
-    o.error_word = _error_word_ptr(error_word)
+    opts = _ROPE_OPTS.pack(bool(interleaved), magnitude, k_scale, v_scale, _error_word_ptr(error_word) or 0)
     keep, refs = _views_of(_ROPE_ARGS, (q_out, q, key, value, positions, inv_freq, slot_mapping, k_cache, v_cache),
                            ("q_out", "q"))
-    _check(_lib.pa_rope_and_cache(*refs, ctypes.byref(o), _stream_handle(stream)), "pa_rope_and_cache")
+    _check(_lib.pa_rope_and_cache(*refs, opts, _stream_handle(stream)), "pa_rope_and_cache")
 
 
 def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,

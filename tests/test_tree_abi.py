@@ -269,6 +269,8 @@ def test_rope_opts_layout(tmp_path):
     subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", exe], check=True)
     got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
     assert got == [ctypes.sizeof(pa.PaRopeOpts)] + [getattr(pa.PaRopeOpts, n).offset for n in fields]
+    packed = pa.PaRopeOpts.from_buffer_copy(pa._ROPE_OPTS.pack(True, 1.5, 0.25, 0.5, 1 << 40))
+    assert [getattr(packed, n) for n in fields] == [1, 1.5, 0.25, 0.5, 1 << 40]
 
 
 def test_frequencies():
