@@ -15,6 +15,10 @@
 // pairs, pass-through, values), so that neighbouring threads always touch neighbouring chunks. A thread
 // takes the same unit of every head that it works on, and so keeps its sines in registers. The loads of
 // its first heads are issued before the sines are made.
+//
+// Measured (B200): 16384 tokens of 32/8 heads of 128, bf16, 403 MB in 68 us (5.9 TB/s, 90% of the measured
+// copy rate); 4097 tokens of 64/8 heads, half of each interleaved, e4m3 pages, 159 MB in 35 us. With 128
+// threads 80 us, with 3 passes in flight 73; one warp to a token 77.
 #include <algorithm>
 
 #include "internal.h"

@@ -5,15 +5,25 @@
 // the keys with a running maximum and sum. A mask touches only the keys past `start`, at most five key
 // blocks at the end of a context: every other block is a dense product.
 //
-// Work. An item is a tile of up to 128 rows of one (sequence, KV head), a unit of it 64 keys (4 pages): the
-// equal spans of tree_sched.cuh, one to each of two CTAs per SM. At most 16 rows: tree_few.cu.
+// Work. An item is NT tiles of 128 rows of one (sequence, KV head), a unit of it 64 keys (4 pages); the
+// spans of tree_sched.cuh go one to a CTA. NT = 1, two CTAs to an SM: one's softmax overlaps the other's
+// products. NT = 2 where a KV head has more than 128 rows: one CTA to an SM, whose two tiles share each
+// block's pages (half the copies, and with e4m3 half the widening) and overlap one another. Measured, 16
+// sequences of 8192 tokens, 32/8 heads: 132 rows 201 us (NT = 1) and 159 (NT = 2), 256 rows 220 and 180,
+// 400 rows 423 and 324; with e4m3 pages 196 and 150, 210 and 171, 406 and 302. At most 16 rows go to
+// tree_few.cu.
 //
 // Per block, as in the prefill kernel: S = Q K^T (tcgen05, K-major operands in 128-byte-swizzled shared
-// memory, two S buffers in tensor memory), softmax by 4 warps with a row per thread, P over S in tensor
-// memory, O += P V (A from tensor memory). Warps: 0-3 softmax, Q loads and epilogue; 4 TMA producer of K;
-// 5 QK issuer and owner of the tensor memory; 6 TMA producer of V; 7 PV issuer. e4m3 pages land as they
-// are (warp 4 brings both) and two pairs of warps widen them into the f16 operand tiles (8-9 K, 10-11 V).
-// Two CTAs per SM.
+// memory, two S buffers in tensor memory), softmax by 4 warps to a tile with a row per thread, P over S in
+// tensor memory, O += P V (A from tensor memory). Warps: 4 NT softmax warps, which also load Q and write
+// the rows; then a TMA producer of K, which walks the schedule and hands its parts to the others, a QK
+// issuer (owner of the tensor memory), a TMA producer of V, a PV issuer. e4m3 pages land as they are (the
+// first producer brings both) and two pairs of warps widen them into the f16 operand tiles.
+//
+// What bounds it (B200): up to about 64 rows the pages' read: 64 sequences of 128 .. 8192 tokens, 64 rows,
+// bf16, 1.25 GB in 221 us (5.66 TB/s; the floor is 191), at the GPU's power limit (1000 W, SM clock 1.6
+// GHz). With more rows the softmax between two products: 8 sequences of 32K .. 128K tokens, 256 rows, e4m3,
+// 584 GFLOP in 622 us (940 TFLOP/s, at the power limit; 528 us in a single call).
 #include <algorithm>
 #include <type_traits>
 

