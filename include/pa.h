@@ -305,20 +305,22 @@ int pa_rope_inv_freq(float* out, int32_t rot_dim, double base, int32_t scaling, 
  *                 E4M3 cache, where q must lie within the f16 range), last stride 1, 16-B aligned rows. Rows
  *                 query_start[s] .. query_start[s + 1] - 1 are sequence s's n_s nodes, whose keys and values
  *                 are the last n_s of its context_lens[s] cached tokens, in node order (write them first).
- *                 Rows outside every sequence are neither read nor written.
+ *                 Rows outside every sequence are neither read nor written. out may be q itself (same
+ *                 strides).
  *   k_cache, v_cache, block_tables  as in pa_decode (E4M3 with D = 128); query_start [B + 1] I32,
  *                 context_lens [B] I32 as in pa_prefill.
  *   tree_mask     [T, W] device I64, contiguous: bit j % 64 of word j / 64 of a node's row is set when
  *                 the node sees node j of its sequence (itself included, where it does); bits at j >= n_s
  *                 are ignored. n_s <= 64 W, W <= 4. NULL: a chain, node i sees nodes 0 .. i.
  *   max_query_len host-known bound on n_s, <= 256 (<= 64 W with a mask).
- *   softcap       0: none; > 0: a scaled score s becomes softcap * tanh(s / softcap).
+ *   softcap       0: none; > 0, <= 1024: a scaled score s becomes softcap * tanh(s / softcap), to 2^-20 of
+ *                 softcap.
  *   opts          k_scale, v_scale, max_context_len, workspace (pa_decode_tree_workspace_bytes) and
  *                 error_word as in pa_decode; partition_tokens must be 0, kernel and prefix_kernel -1.
  * Every node sees all of the first context_lens[s] - n_s tokens, and of the drafted ones those that its
  * mask names: out = softmax(scale * q K^T) V over what it sees, float32 accumulation, rounded to nearest
- * even; a node that sees nothing gives zeros. Cached rows that no bit makes visible to a node may hold
- * anything, infinities and NaN included, without reaching that node's row.
+ * even; a node that sees nothing (or whose every score is -infinity) gives zeros. Cached rows that no bit
+ * makes visible to a node may hold anything, infinities and NaN included, without reaching that node's row.
  * A sequence that only the device can see is out of contract (n_s < 0, > max_query_len or
  * > context_lens[s], a context longer than max_context_len or the table, rows outside q) sets
  * PA_DEVERR_CTX_RANGE and its rows are left as they were; a bad block id sets PA_DEVERR_BAD_BLOCK and that
@@ -329,14 +331,16 @@ int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache,
                    const pa_tensor* tree_mask, int32_t max_query_len, float scale, float softcap,
                    int32_t num_kv_heads, const pa_decode_opts* opts, void* stream);
 
-/* Workspace bytes pa_decode_tree needs for these sizes (0 when no context is split). Host only. */
+/* Workspace bytes that a pa_decode_tree call of these sizes asks for, and that do for every call of smaller ones
+ * (0 when no context is split; a call's max_context_len counts, or the table's width where that is 0). Calls that
+ * may overlap on the GPU need workspaces of their own. Host only. */
 size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                       int32_t max_query_len, int32_t max_context_len);
 
 /*
  * pa_commit_tree -- keep the accepted path of each sequence's drafted tree.
  *   k_cache, v_cache  [num_blocks, Hkv, 16, D] contiguous, any one dtype of F16, BF16 and E4M3; a row
- *                     (D elements) a multiple of 16 bytes.
+ *                     (D elements) a multiple of 16 bytes; two pools, not one given twice.
  *   block_tables, query_start, context_lens  as pa_decode_tree had them (n_s <= 256 drafted nodes at the end
  *                     of context_lens[s] tokens; query_start's differences alone matter).
  *   accepted          [B, P] device I32, last stride 1: the accepted nodes in path order, strictly

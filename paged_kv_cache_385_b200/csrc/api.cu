@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <climits>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -114,6 +115,21 @@ bool overlap(const pa_tensor* a, const pa_tensor* b) {
     hi[k] = lo[k] + static_cast<uintptr_t>(bytes);
   }
   return lo[0] < hi[1] && lo[1] < hi[0];
+}
+
+// Whether b starts where a does but lies otherwise: not a pair for work in place.
+bool skewed(const pa_tensor* a, const pa_tensor* b) {
+  if (a->data != b->data) return false;
+  for (int i = 0; i < a->ndim; ++i)
+    if (a->shape[i] > 1 && a->stride[i] != b->stride[i]) return true;
+  return false;
+}
+
+// The first of these whose data is not aligned to its elements, or null.
+const pa_tensor* misaligned(std::initializer_list<const pa_tensor*> tensors) {
+  for (const pa_tensor* t : tensors)
+    if (t && !aligned(t->data, static_cast<uintptr_t>(elem_bytes(t->dtype)))) return t;
+  return nullptr;
 }
 
 // ---- TMA descriptor encoding -----------------------------------------------------------------
@@ -253,6 +269,19 @@ size_t tree_workspace(int64_t head_dim, const pa::TreePlan& plan, size_t* ml_off
   if (ml_offset) *ml_offset = acc;
   if (desc_offset) *desc_offset = acc + ml;
   return acc + ml + round_up(static_cast<size_t>(plan.spans) * pa::kTreeDescInts * sizeof(int32_t), 256);
+}
+
+// The most that any call of at most these sizes needs, which is what a call asks for: fewer nodes may take a
+// form with more spans, so that what the sizes themselves need would not grow with them.
+size_t tree_workspace_of(int64_t head_dim, int64_t num_seqs, int num_kv_heads, int group, int max_query_len,
+                         int64_t max_context_len) {
+  size_t most = 0;
+  for (const int rows : {pa::kTreeFewRows / 2, pa::kTreeFewRows, pa::kTreeRows, INT_MAX}) {
+    const int nodes = std::min(max_query_len, std::max(1, rows / group));
+    most = std::max(most, tree_workspace(head_dim, pa::tree_plan(num_seqs, num_kv_heads, group, nodes, max_context_len),
+                                         nullptr, nullptr));
+  }
+  return most;
 }
 
 }  // namespace
@@ -960,6 +989,9 @@ int pa_rope_and_cache(pa_tensor* q_out, const pa_tensor* q, const pa_tensor* key
     return fail(PA_ERR_INVALID_ARG, "caches must be 16-byte aligned");
   if (!positions->data || !inv_freq->data || !slot_mapping->data || !k_cache->data || !v_cache->data)
     return fail(PA_ERR_INVALID_ARG, "NULL data pointer");
+  if (misaligned({positions, inv_freq, slot_mapping}) || !aligned(opts.error_word, 4))
+    return fail(PA_ERR_INVALID_ARG, "positions, inv_freq, slot_mapping and error_word must be aligned to their elements");
+  if (q && skewed(q, q_out)) return fail(PA_ERR_INVALID_ARG, "in place, q_out must have q's strides");
 
   pa::RopeParams p{};
   p.key = key->data;
@@ -1013,8 +1045,7 @@ size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int
   if (num_seqs <= 0 || num_kv_heads <= 0 || num_q_heads < num_kv_heads || head_dim <= 0 || max_query_len <= 0 ||
       max_context_len <= 0)
     return 0;
-  return tree_workspace(head_dim, pa::tree_plan(num_seqs, num_kv_heads, num_q_heads / num_kv_heads, max_query_len, max_context_len),
-                        nullptr, nullptr);
+  return tree_workspace_of(head_dim, num_seqs, num_kv_heads, num_q_heads / num_kv_heads, max_query_len, max_context_len);
 }
 
 int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
@@ -1063,6 +1094,8 @@ int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache,
   }
   if (!std::isfinite(scale)) return fail(PA_ERR_INVALID_ARG, "scale must be finite");
   if (!(std::isfinite(softcap) && softcap >= 0.f)) return fail(PA_ERR_INVALID_ARG, "softcap must be finite and >= 0");
+  // (A capped score is right to 2^-20 of the cap: larger caps would cost the weights more than their rounding.)
+  if (softcap > 1024.f) return fail(PA_ERR_UNSUPPORTED, "softcap %g exceeds 1024", static_cast<double>(softcap));
   if (T == 0 || B == 0 || Hq == 0) return ok();
   if (max_query_len <= 0) return fail(PA_ERR_INVALID_ARG, "max_query_len must be > 0");
   if (max_query_len > pa::kTreeMaxNodes || (tree_mask && max_query_len > 64 * tree_mask->shape[1]))
@@ -1086,7 +1119,10 @@ int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache,
   if (!out->data || !q->data || !k_cache->data || !v_cache->data || !block_tables->data || !query_start->data ||
       !context_lens->data || (tree_mask && !tree_mask->data))
     return fail(PA_ERR_INVALID_ARG, "NULL data pointer");
-  if (tree_mask && !aligned(tree_mask->data, 8)) return fail(PA_ERR_INVALID_ARG, "tree_mask must be 8-byte aligned");
+  if (tree_mask && misaligned({tree_mask})) return fail(PA_ERR_INVALID_ARG, "tree_mask must be 8-byte aligned");
+  if (misaligned({block_tables, query_start, context_lens}) || !aligned(opts.error_word, 4))
+    return fail(PA_ERR_INVALID_ARG, "block_tables, query_start, context_lens and error_word must be 4-byte aligned");
+  if (skewed(q, out)) return fail(PA_ERR_INVALID_ARG, "in place, out must have q's strides");
   float k_scale = 1.f, v_scale = 1.f;
   if (cd == PA_E4M3) {
     k_scale = opts.k_scale;
@@ -1094,6 +1130,7 @@ int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache,
     if (!(std::isfinite(k_scale) && k_scale > 0.f && std::isfinite(v_scale) && v_scale > 0.f))
       return fail(PA_ERR_INVALID_ARG, "E4M3 cache scales must be finite and > 0");
   }
+  if (!std::isfinite(scale * k_scale * 2.f)) return fail(PA_ERR_INVALID_ARG, "scale * k_scale overflows");
   if (opts.max_context_len < 0) return fail(PA_ERR_INVALID_ARG, "max_context_len < 0");
   if (opts.partition_tokens != 0 || opts.kernel != -1 || opts.prefix_kernel != -1)
     return fail(PA_ERR_INVALID_ARG, "pa_decode_tree splits contexts and picks its kernel itself: partition_tokens must be "
@@ -1132,7 +1169,8 @@ int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache,
   p.tile_rows = plan.rows;
   p.spans = plan.spans;
   size_t ml_off = 0, desc_off = 0;
-  if (const size_t need = tree_workspace(D, plan, &ml_off, &desc_off)) {
+  if (tree_workspace(D, plan, &ml_off, &desc_off)) {
+    const size_t need = tree_workspace_of(D, B, p.num_kv_heads, p.group, max_query_len, max_ctx);
     const size_t have = opts.workspace ? opts.workspace_bytes : 0;
     if (have < need)
       return fail(PA_ERR_WORKSPACE, "contexts of up to %lld tokens need a workspace of %zu bytes (got %zu)", (long long)max_ctx,
@@ -1200,8 +1238,12 @@ int pa_commit_tree(pa_tensor* k_cache, pa_tensor* v_cache, const pa_tensor* bloc
   if (!k_cache->data || !v_cache->data || !block_tables->data || !query_start->data || !context_lens->data ||
       !accepted_lens->data || (accepted->shape[1] > 0 && !accepted->data) || (new_context_lens && !new_context_lens->data))
     return fail(PA_ERR_INVALID_ARG, "NULL data pointer");
+  if (misaligned({block_tables, query_start, context_lens, accepted, accepted_lens, new_context_lens}) || !aligned(error_word, 4))
+    return fail(PA_ERR_INVALID_ARG, "lengths, tables, paths and error_word must be aligned to their elements");
+  // (Rows move by several CTAs: one pool given twice would be read while it is written.)
+  if (overlap(k_cache, v_cache)) return fail(PA_ERR_INVALID_ARG, "k_cache and v_cache overlap");
   if (new_context_lens) {
-    const pa_tensor* ins[5] = {block_tables, query_start, context_lens, accepted, accepted_lens};
+    const pa_tensor* ins[7] = {block_tables, query_start, context_lens, accepted, accepted_lens, k_cache, v_cache};
     for (const pa_tensor* t : ins)
       if (overlap(new_context_lens, t)) return fail(PA_ERR_INVALID_ARG, "new_context_lens overlaps another argument");
   }

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap, NT>::kThreads, NT == 2 ? 1
     constexpr int kPages = kKeys / 16;
     constexpr uint32_t kBytes = L::kFp8 ? L::kRawTile : L::kTile;  // 128-byte rows, one or two per key
     const int oob_row = p.num_blocks * p.num_kv_heads * 16;        // a box starting here is all zero fill
-    const int npages = (P->ctx + 15) / 16, hk = P->hk, j1 = P->j1;
+    const int npages = (P->ctx - 1) / 16 + 1, hk = P->hk, j1 = P->j1;
     const int32_t* bt = p.block_tables + static_cast<int64_t>(P->s) * p.bt_stride;
     int ids[kPages];  // the block's page ids, loaded a block ahead
     auto fetch = [&](int j) {
@@ -465,13 +465,14 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap, NT>::kThreads, NT == 2 ? 1
     const int s_full = kSFull0 + 2 * t, p_full = kPFull0 + 2 * t, o_done = kODone0 + 2 * t;
     const int G = p.group;
     const uint32_t inv_g = (65536u + G - 1) / G;
-    // A negative scale turns Q's sign (load_q), so that the largest product gives the largest score.
+    // A negative scale turns Q's sign (finish_q), so that the largest product gives the largest score.
     const bool negate = p.score_scale < 0.f;
     // (A scale of 0 becomes one that makes every finite score 0 and leaves a masked score's -inf.)
     const float sl2 = fmaxf(fabsf(p.score_scale) * 1.4426950408889634f, 1e-37f);
     // Capped scores: cap * tanh(s / cap) = cap - 2 cap / (1 + 2^(u s)), in log2 units.
     const float cap2 = kCap ? p.softcap * 1.4426950408889634f : 0.f;
-    const float cap_u = kCap ? 2.f * sl2 / p.softcap : 0.f;
+    // (Of a cap so small that u would overflow, u's sign alone matters.)
+    const float cap_u = kCap ? fminf(2.f * sl2 / p.softcap, 1e30f) : 0.f;
     volatile uint32_t* bad_nodes = reinterpret_cast<volatile uint32_t*>(smem + L::kBarOff + 8 * kBadNodes);
     int meets = 0;
     if (threadIdx.x == 0) tree::describe_none(p, blockIdx.x);
@@ -791,8 +792,9 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap, NT>::kThreads, NT == 2 ? 1
 #pragma unroll 1
               for (uint32_t bits = bad_nodes[w]; bits; bits &= bits - 1) {
                 const int nd = 32 * w + __ffs(bits) - 1, at_token = P->start + nd;
-                if (!(tree::mask_word(p, P, node, nd >> 6) >> (nd & 63) & 1ull)) continue;
-                const int64_t at = ((static_cast<int64_t>(bt[at_token >> 4]) * p.num_kv_heads + P->hk) * 16 + (at_token & 15)) * D + c * 32;
+                const int id = bt[at_token >> 4];
+                if (id < 0 || id >= p.num_blocks || !(tree::mask_word(p, P, node, nd >> 6) >> (nd & 63) & 1ull)) continue;
+                const int64_t at = ((static_cast<int64_t>(id) * p.num_kv_heads + P->hk) * 16 + (at_token & 15)) * D + c * 32;
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
                   if constexpr (L::kFp8) {

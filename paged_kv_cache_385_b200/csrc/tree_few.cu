@@ -209,7 +209,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, OCC)
   RowMath<C, D, NT, kCap> rows;
   rows.lane = lane;
   const float log2e = 1.4426950408889634f;
-  const float sl2 = kCap ? 2.f * p.score_scale / p.softcap * log2e : p.score_scale * log2e;
+  // (Of a cap so small that the factor would overflow, its sign alone matters.)
+  const float sl2 = kCap ? fmaxf(fminf(2.f * p.score_scale / p.softcap * log2e, 1e30f), -1e30f) : p.score_scale * log2e;
   const float cap2 = kCap ? p.softcap * log2e : 0.f;
   int consumed = 0;
   bool ok = true;

@@ -44,7 +44,7 @@ __device__ __forceinline__ Seq load_seq(const TreeParams& p, int s, bool* bad) {
   q.n = *bad ? 0 : static_cast<int>(n);
   q.rows = q.n * p.group;
   q.tiles = (q.rows + Pol::kRows - 1) / Pol::kRows;
-  q.units = q.n ? (q.ctx + Pol::kTokens - 1) / Pol::kTokens : 0;
+  q.units = q.n ? (q.ctx - 1) / Pol::kTokens + 1 : 0;
   return q;
 }
 

@@ -50,6 +50,9 @@ CASES = {
     "capped_e4m3": ("e4m3", 128, 1, 8, [20], [300], {"softcap": 5.0}),
     "negative_scale": ("f16", 128, 1, 4, [9, 2], [150, 40], {"scale": -0.08}),
     "zero_scale": ("bf16", 128, 1, 4, [9], [150], {"scale": 0.0}),
+    "zero_scale_few": ("f16", 128, 1, 2, [3], [150], {"scale": 0.0}),
+    "tiny_cap": ("f16", 128, 1, 4, [9], [150], {"softcap": 1e-38}),
+    "tiny_cap_few": ("bf16", 128, 1, 1, [9], [150], {"softcap": 1e-38, "scale": -1.0}),
     "long_split": ("bf16", 128, 1, 4, [10], [9001], {}),
     "long_split_e4m3": ("e4m3", 128, 1, 8, [3], [8000], {}),
     "long_split_d64": ("f16", 64, 2, 1, [5, 2], [7000, 33], {}),
@@ -186,6 +189,42 @@ def test_placement_and_repetition_change_nothing(kv, counts):
         assert torch.equal(a.run(workspace=a.workspace(fill)), first)
     b = TreeCase(*args, seed=10, order=99).to_device()
     assert torch.equal(b.run(), first)
+
+
+@pytest.mark.parametrize("counts", [[9, 40, 3], [2, 1, 4]])
+def test_in_place(counts):
+    """Contexts that are split and whole ones: every row's query is read before the row is written."""
+    c = TreeCase("bf16", 128, 2, 4, counts, [9000, 90, 200], seed=16).to_device()
+    want = c.run().clone()
+    q = c.q.clone()
+    c.run(out=q, q=q)
+    T = sum(counts)
+    assert torch.equal(q[:T], want[:T])
+
+
+@pytest.mark.parametrize("kv,group", [("f16", 4), ("f16", 1), ("bf16", 4), ("e4m3", 8)])
+def test_the_largest_cap(kv, group):
+    """A capped score is off by at most 2^-20 of the cap: at 1024, 2^-10 on each weight and on their sum."""
+    c = TreeCase(kv, 128, 2, group, [9, 7], [700, 64], seed=17, softcap=1024.0).to_device()
+    got = c.run()
+    want, weight = c.oracle()
+    T = sum(c.counts)
+    off = np.abs(got.double().cpu().numpy()[:T] - want[:T])
+    assert np.all(off <= c.bound(want, weight)[:T] + 2 * 2.0 ** -10 * weight[:T])
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on the GPU, each with its own workspace."""
+    a = TreeCase("bf16", 128, 2, 4, [16, 5], [9000, 4000], seed=18).to_device()
+    b = TreeCase("e4m3", 128, 2, 1, [7, 5, 3], [8000, 90, 2000], seed=19).to_device()
+    runs = [(c, c.run().clone(), c.workspace(), torch.cuda.Stream(), torch.full_like(c.out, 77.0)) for c in (a, b)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, _, ws, stream, out in runs:
+            c.run(out=out, workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    for c, want, _, _, out in runs:
+        assert torch.equal(out, want)
 
 
 def test_default_context_bound_is_the_table():

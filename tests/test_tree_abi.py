@@ -175,6 +175,14 @@ def test_tree_workspace():
     assert need > 0 and need % 256 == 0
     assert pa.pa_decode_tree_workspace_bytes(2, 4, 2, 128, 5, 64) == 0  # one key block: nothing to split
     assert pa.pa_decode_tree_workspace_bytes(0, 4, 2, 128, 5, 4096) == 0
+    r = random.Random(0)  # sized once for the largest, it does for every smaller call
+    for _ in range(300):
+        group, hkv, d = r.choice([1, 3, 4, 8, 16]), r.choice([1, 8, 32]), r.choice([64, 128])
+        b, n, c = r.randint(1, 300), r.randint(1, 256), r.choice([60, 129, 250, 260, 3000, 131072])
+        most = pa.pa_decode_tree_workspace_bytes(b, group * hkv, hkv, d, n, c)
+        for _ in range(5):
+            less = pa.pa_decode_tree_workspace_bytes(r.randint(1, b), group * hkv, hkv, d, r.randint(1, n), r.randint(1, c))
+            assert less <= most, (b, group, hkv, d, n, c)
     a = tree_args(bt=aligned_zeros((2, 4096), I32))
     ws = aligned_zeros((need + 256,), torch.uint8)
     assert attend(a) == pa.PA_ERR_WORKSPACE
@@ -213,6 +221,54 @@ def test_commit_overlaps_and_empty_calls():
                         **{n: aligned_zeros((0,), I32) for n in ("lens", "accepted_lens", "new")},
                         accepted=aligned_zeros((0, 3), I32))
     assert commit(empty) == pa.PA_OK
+
+
+def moved(args, name, by):
+    """args with one tensor's data moved by some bytes."""
+    t = pa.as_pa_tensor(args[name], name, device=False)
+    t.data += by
+    return {**args, name: t}
+
+
+@cpu_only
+@pytest.mark.parametrize("make,call,names", [
+    (rope_args, rope, ("positions", "inv_freq", "slots")), (tree_args, attend, ("bt", "start", "lens")),
+    (commit_args, commit, ("bt", "start", "lens", "accepted", "accepted_lens", "new"))])
+def test_unaligned_index_tensors_are_refused(make, call, names):
+    held = make()
+    for name in names:
+        for by in (1, 2, 3):
+            assert call(moved(held, name, by)) == INVALID and "aligned" in pa.pa_last_error(), name
+    if call is commit:
+        return
+    word = aligned_zeros((2,), I32)
+    assert call(held, error_word=word.data_ptr() + 2) == INVALID and "aligned" in pa.pa_last_error()
+    assert call(held, error_word=word.data_ptr()) == pa.PA_ERR_CUDA
+
+
+@cpu_only
+def test_pairs_in_one_place():
+    """Queries may be worked on in place, with their own strides; commit's two pools may not be one."""
+    wide = aligned_zeros((5, 4, 256), BF)[..., :128]
+    tight = wide.as_strided((5, 4, 128), (512, 128, 1))
+    assert attend(tree_args(out=wide, q=wide)) == pa.PA_ERR_CUDA
+    assert attend(tree_args(out=wide, q=tight)) == INVALID and "in place" in pa.pa_last_error()
+    assert rope(rope_args(q=wide[:3], q_out=wide[:3])) == pa.PA_ERR_CUDA
+    assert rope(rope_args(q=wide[:3], q_out=tight[:3])) == INVALID and "in place" in pa.pa_last_error()
+    pools = aligned_zeros((2, 8, 2, 16, 128), BF)
+    assert commit(commit_args(k_cache=pools[0], v_cache=pools[1])) == pa.PA_ERR_CUDA
+    assert commit(commit_args(k_cache=pools[0], v_cache=pools[0])) == INVALID and "overlap" in pa.pa_last_error()
+    both = aligned_zeros((9, 2, 16, 128), BF)
+    assert commit(commit_args(k_cache=both[:8], v_cache=both[1:])) == INVALID
+
+
+@cpu_only
+def test_scales_and_caps_out_of_range():
+    assert attend(tree_args(), scale=3e38) == INVALID and "overflows" in pa.pa_last_error()
+    e4 = tree_args(k_cache=aligned_zeros((8, 2, 16, 128), E4), v_cache=aligned_zeros((8, 2, 16, 128), E4))
+    assert attend(e4, scale=1e20, k_scale=1e20) == INVALID
+    assert attend(tree_args(), cap=1024.5) == UNSUPPORTED and "1024" in pa.pa_last_error()
+    assert attend(tree_args(), cap=1024.0) == pa.PA_ERR_CUDA
 
 
 @cpu_only
