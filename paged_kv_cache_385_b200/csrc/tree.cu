@@ -148,6 +148,14 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // R / G for R < 4096 and G <= 16, by a multiplication: inv_g = ceil(65536 / G).
 __device__ __forceinline__ int div_group(int R, uint32_t inv_g) { return static_cast<int>((R * inv_g) >> 16); }
 
+// 16 bytes of shared memory.
+__device__ __forceinline__ void ld_shared(uint32_t at, uint32_t* w) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+}
+__device__ __forceinline__ void st_shared(uint32_t at, const uint32_t* w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+
 template <KvType KV, bool kQBf16, int D, bool kCap, int NT>
 __global__ void __launch_bounds__(Layout<KV, D, kCap, NT>::kThreads, NT == 2 ? 1 : 2)
     tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const TreeParams p) {
@@ -297,20 +305,23 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap, NT>::kThreads, NT == 2 ? 1
           break;
         }
         const uint32_t raw = base + raw_off + rs * kHalf, dst = base + off + st * L::kTile + dst0;
-#pragma unroll 4
-        for (int i = 0; i < kKeys / 8; ++i) {
-          const int row = (32 * half + (lane >> 3) + 4 * i) ^ (c >> 2);
-          uint32_t w[4], o[8];
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                       : "r"(raw + row * 128 + ((c ^ (row & 7)) << 4)));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2x2(w[k], o[2 * k], o[2 * k + 1]);
+        for (int i0 = 0; i0 < kKeys / 8; i0 += 4) {
+          uint32_t w[4][4];  // (loaded before any is stored: their latencies overlap)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + row * 128 + (((e + h) ^ (row & 7)) << 4)),
-                         "r"(o[4 * h]), "r"(o[4 * h + 1]), "r"(o[4 * h + 2]), "r"(o[4 * h + 3])
-                         : "memory");
+          for (int i = 0; i < 4; ++i) {
+            const int row = (32 * half + (lane >> 3) + 4 * (i0 + i)) ^ (c >> 2);
+            ld_shared(raw + row * 128 + ((c ^ (row & 7)) << 4), w[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = (32 * half + (lane >> 3) + 4 * (i0 + i)) ^ (c >> 2);
+            uint32_t o[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2x2(w[i][k], o[2 * k], o[2 * k + 1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) st_shared(dst + row * 128 + (((e + h) ^ (row & 7)) << 4), o + 4 * h);
+          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -513,45 +524,54 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap, NT>::kThreads, NT == 2 ? 1
     // the tensor cores less power, and these kernels run into the GPU's power limit). start_q may run once
     // the QKs of the part before have (this warp has seen its last S), finish_q hands the tile to the QK
     // issuer.
-    constexpr int kRowChunks = D / 8;
-    auto q_addr = [&](int x) -> uint32_t {
-      const int row = quad * 32 + x / kRowChunks, c = x % kRowChunks;
-      return base + L::kQOff + t * L::kQTile + (c >> 3) * kQHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+    constexpr int kRowChunks = D / 8, kAtOnce = 32 / kRowChunks, kSteps = 8 / kAtOnce;  // rows of a step; steps of 8 rows
+    const int q_row = lane / kRowChunks, q_col = lane % kRowChunks;
+    const uint32_t q_tile = base + L::kQOff + t * L::kQTile + (q_col >> 3) * kQHalf + quad * 32 * 128;
+    auto q_addr = [&](int i, int k) -> uint32_t {  // of this lane's chunk in step k of the warp's rows 8 i .. 8 i + 7
+      const int row = q_row + kAtOnce * k;
+      return q_tile + i * 1024 + row * 128 + (((q_col & 7) ^ row) << 4);
     };
     auto start_q = [&](const volatile Part* P) {
       const int row0 = P->tile * kItemRows + t * kRows, left = min(P->rows - row0, kRows);
-      const int head0 = P->hk * G, c = lane % kRowChunks;
       const int from = (quad * 32 - turn_of(left)) & (kRows - 1);  // the warp's first row of the tile
-      const uint16_t* q0 = static_cast<const uint16_t*>(p.q) + P->q0 * p.q_stride_t + c * 8;
-#pragma unroll 4
-      for (int x = lane; x < 32 * kRowChunks; x += 32) {
-        const int row = from + x / kRowChunks;
-        if (row >= left) {
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(q_addr(x)), "r"(0u) : "memory");
-          continue;
+      // Row R = node * G + g lies at node * stride_t + g * stride_h = R * stride_h + node * wrap.
+      const int64_t sh = p.q_stride_h, wrap = p.q_stride_t - G * sh;
+      const uint16_t* q0 = static_cast<const uint16_t*>(p.q) + P->q0 * p.q_stride_t + (P->hk * G + row0 + from) * sh + q_col * 8;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          const int row = 8 * i + q_row + kAtOnce * k;
+          if (from + row < left) {
+            const uint16_t* src = q0 + row * sh + div_group(row0 + from + row, inv_g) * wrap;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(q_addr(i, k)), "l"(src) : "memory");
+          } else {
+            const uint32_t zeros[4] = {0u, 0u, 0u, 0u};
+            st_shared(q_addr(i, k), zeros);
+          }
         }
-        const int R = row0 + row, node = div_group(R, inv_g);
-        const uint16_t* src = q0 + node * p.q_stride_t + (head0 + R - node * G) * p.q_stride_h;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(q_addr(x)), "l"(src) : "memory");
       }
     };
     auto finish_q = [&] {
       asm volatile("cp.async.wait_all;" ::: "memory");
       if ((kQBf16 && !kBf16) || negate) {  // this lane's own chunks: bf16 to f16, and the sign
-#pragma unroll 4
-        for (int x = lane; x < 32 * kRowChunks; x += 32) {
-          uint32_t w[4];
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(q_addr(x)));
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[kSteps][4];  // (loaded before any is stored: their latencies overlap)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (negate) w[i] ^= 0x80008000u;
-            if constexpr (kQBf16 && !kBf16) {
-              const float2 f = unpack2<true>(w[i]);
-              w[i] = pack2<false>(f.x, f.y);
+          for (int k = 0; k < kSteps; ++k) ld_shared(q_addr(i, k), w[k]);
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (negate) w[k][e] ^= 0x80008000u;
+              if constexpr (kQBf16 && !kBf16) {
+                const float2 f = unpack2<true>(w[k][e]);
+                w[k][e] = pack2<false>(f.x, f.y);
+              }
             }
+            st_shared(q_addr(i, k), w[k]);
           }
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(q_addr(x)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                       : "memory");
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -594,18 +614,27 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap, NT>::kThreads, NT == 2 ? 1
         const uint32_t tS = tS0 + (gb & 1) * kKeys;
         // The block's largest score in log2 units: cap and scale are monotone, so they are applied to the
         // largest raw score alone.
-        float sv[L::kHeld], top = -INFINITY;
-        if constexpr (L::kHeld == kKeys) tc05::ld64(tS, sv);
+        float top = -INFINITY, held[kMasked ? 1 : L::kHeld];
+        if constexpr (kMasked) {
+#pragma unroll 1
+          for (int h = 0; h < kKeys / 16; ++h) {
+            float x[16];
+            tc05::ld16(tS + 16 * h, x);
+            const uint32_t bits = static_cast<uint32_t>(vis >> (16 * h));
 #pragma unroll
-        for (int h = 0; h < kKeys / L::kHeld; ++h) {
-          if constexpr (L::kHeld == 32) tc05::ld32(tS + 32 * h, sv);
-          if constexpr (kMasked) {
-            const uint64_t bits = vis >> (32 * h);
-#pragma unroll
-            for (int k = 0; k < L::kHeld; ++k)
-              if (!(static_cast<uint32_t>(bits >> (k & 32)) >> (k & 31) & 1u)) sv[k] = -INFINITY;
+            for (int k = 0; k < 16; ++k)
+              if (!(bits >> k & 1u)) x[k] = -INFINITY;
+            top = fmaxf(top, largest(x));
           }
-          top = fmaxf(top, largest(sv));
+        } else if constexpr (L::kHeld == kKeys) {
+          tc05::ld64(tS, held);
+          top = largest(held);
+        } else {
+#pragma unroll
+          for (int h = 0; h < kKeys / 32; ++h) {
+            tc05::ld32(tS + 32 * h, held);
+            top = fmaxf(top, largest(held));
+          }
         }
         const float mx = kMasked && vis == 0ull ? -INFINITY : score(top);
         // (Each row raises its own reference, so that its result does not depend on its neighbours'.)
@@ -618,24 +647,39 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap, NT>::kThreads, NT == 2 ? 1
         }
         const float nref = L::kShift - (m == -INFINITY ? 0.f : m);
         float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        if constexpr (kMasked) {
+          // (P of a quarter lies over scores that are read already.)
+#pragma unroll 1
+          for (int h = 0; h < kKeys / 16; ++h) {
+            float x[16];
+            tc05::ld16(tS + 16 * h, x);
+            const uint32_t bits = static_cast<uint32_t>(vis >> (16 * h));
+            uint32_t wd[8];
 #pragma unroll
-        for (int h = 0; h < kKeys / 32; ++h) {
-          // (P of the first half lies over that half's scores: the second's are still there.)
-          if constexpr (L::kHeld == 32) tc05::ld32(tS + 32 * h, sv);
-          float* x = sv + (L::kHeld == 32 ? 0 : 32 * h);
-          const uint32_t bits = static_cast<uint32_t>(vis >> (32 * h));
-          uint32_t wd[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            weights(x[2 * k], x[2 * k + 1], nref);
-            if constexpr (kMasked && (kCap || L::kHeld == 32)) {  // (else the score is -inf already)
+            for (int k = 0; k < 8; ++k) {
+              weights(x[2 * k], x[2 * k + 1], nref);
               if (!(bits >> (2 * k) & 1u)) x[2 * k] = 0.f;
               if (!(bits >> (2 * k + 1) & 1u)) x[2 * k + 1] = 0.f;
+              rs[k & 3] = add2(rs[k & 3], make_float2(x[2 * k], x[2 * k + 1]));
+              wd[k] = pack2<kBf16>(x[2 * k], x[2 * k + 1]);
             }
-            rs[k & 3] = add2(rs[k & 3], make_float2(x[2 * k], x[2 * k + 1]));
-            wd[k] = pack2<kBf16>(x[2 * k], x[2 * k + 1]);
+            tc05::st8u_nowait(tS + 8 * h, wd);
           }
-          tc05::st16u_nowait(tS + 16 * h, wd);
+        } else {
+#pragma unroll
+          for (int h = 0; h < kKeys / 32; ++h) {
+            // (P of the first half lies over that half's scores: the second's are still there.)
+            if constexpr (L::kHeld == 32) tc05::ld32(tS + 32 * h, held);
+            float* x = held + (L::kHeld == 32 ? 0 : 32 * h);
+            uint32_t wd[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              weights(x[2 * k], x[2 * k + 1], nref);
+              rs[k & 3] = add2(rs[k & 3], make_float2(x[2 * k], x[2 * k + 1]));
+              wd[k] = pack2<kBf16>(x[2 * k], x[2 * k + 1]);
+            }
+            tc05::st16u_nowait(tS + 16 * h, wd);
+          }
         }
         const float2 sum = add2(add2(rs[0], rs[1]), add2(rs[2], rs[3]));
         l = l * alpha + (sum.x + sum.y);
@@ -731,24 +775,32 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap, NT>::kThreads, NT == 2 ? 1
           constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u, kLow = kBf16 ? 0x00800080u : 0x04000400u;
           const uint32_t vb = base + L::kVOff + (gb % L::kVStages) * L::kTile;
           const int t0 = j * kKeys, start = P->start, first = max(start - t0, 0), held = P->ctx - t0;
-#pragma unroll 4
-          for (int x = threadIdx.x; x < (kKeys - first) * C; x += 32 * kSoft) {
-            const int row = first + x / C, c = x % C;
-            const uint32_t a = vb + (c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
-            uint32_t odd = 0u;
+#pragma unroll 1
+          for (int x0 = threadIdx.x; x0 < (kKeys - first) * C; x0 += 2 * 32 * kSoft) {
+            uint32_t w[2][4];  // (both loaded before either is stored)
+            const bool two = x0 + 32 * kSoft < (kKeys - first) * C;
+            auto addr = [&](int x) -> uint32_t {
+              const int row = first + x / C, c = x % C;
+              return vb + (c >> 3) * kHalf + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+            };
+            ld_shared(addr(x0), w[0]);
+            if (two) ld_shared(addr(x0 + 32 * kSoft), w[1]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) odd |= (w[i] & kExp) + kLow;
-            if ((odd & 0x80008000u) || row >= held) {
+            for (int i = 0; i < 2; ++i) {
+              if (i == 1 && !two) break;
+              const int x = x0 + i * 32 * kSoft, row = first + x / C;
+              uint32_t odd = 0u;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) w[i] = row < held ? w[i] & ~__vcmpeq2(w[i] & kExp, kExp) : 0u;
-              if (row < held) {
-                const int nd = t0 + row - start;
-                atomicOr(const_cast<uint32_t*>(&bad_nodes[nd >> 5]), 1u << (nd & 31));
+              for (int k = 0; k < 4; ++k) odd |= (w[i][k] & kExp) + kLow;
+              if ((odd & 0x80008000u) || row >= held) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[i][k] = row < held ? w[i][k] & ~__vcmpeq2(w[i][k] & kExp, kExp) : 0u;
+                if (row < held) {
+                  const int nd = t0 + row - start;
+                  atomicOr(const_cast<uint32_t*>(&bad_nodes[nd >> 5]), 1u << (nd & 31));
+                }
+                st_shared(addr(x), w[i]);
               }
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                           : "memory");
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -781,7 +833,7 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap, NT>::kThreads, NT == 2 ? 1
         for (int w = 0; w < 8; ++w) any_bad |= bad_nodes[w];
       }
       if (working) {
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           float v[32];
           tc05::ld32(tO + c * 32, v);
