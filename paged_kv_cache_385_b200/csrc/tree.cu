@@ -57,11 +57,11 @@ struct Layout {
   static constexpr int kHalves = D / 64;
   static constexpr uint32_t kQTile = kHalves * kQHalf;
   static constexpr uint32_t kTile = kHalves * kHalf;
-  static constexpr int kKStages = NT == 2 ? (kFp8 ? 2 : (D == 128 ? 5 : 8)) : (kFp8 ? 1 : (D == 128 ? 3 : 4));
+  static constexpr int kKStages = NT == 2 ? (kFp8 ? 2 : (D == 128 ? 5 : 8)) : (kFp8 ? 2 : (D == 128 ? 3 : 4));
   static constexpr int kVStages = NT == 2 ? kKStages : (kFp8 ? 1 : (D == 128 ? 2 : 4));
   // e4m3: pages land in rings of their own and are widened into the operand tiles.
   static constexpr uint32_t kRawTile = kFp8 ? kHalf : 0;
-  static constexpr int kRawStages = NT == 2 ? 6 : 3;
+  static constexpr int kRawStages = NT == 2 ? 6 : 2;
   static constexpr uint32_t kQOff = 0;
   static constexpr uint32_t kKOff = NT * kQTile;
   static constexpr uint32_t kVOff = kKOff + kKStages * kTile;
