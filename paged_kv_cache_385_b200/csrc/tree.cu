@@ -9,8 +9,8 @@
 // spans of tree_sched.cuh go one to a CTA. NT = 1, two CTAs to an SM: one's softmax overlaps the other's
 // products. NT = 2 where a KV head has more than 128 rows: one CTA to an SM, whose two tiles share each
 // block's pages (half the copies, and with e4m3 half the widening) and overlap one another. Measured, 16
-// sequences of 8192 tokens, 32/8 heads: 132 rows 201 us (NT = 1) and 159 (NT = 2), 256 rows 220 and 180,
-// 400 rows 423 and 324; with e4m3 pages 196 and 150, 210 and 171, 406 and 302. At most 16 rows go to
+// sequences of 8192 tokens, 32/8 heads: 132 rows 197 us (NT = 1) and 155 (NT = 2), 256 rows 231 and 184,
+// 400 rows 427 and 327; with e4m3 pages 179 and 149, 205 and 172, 383 and 305. At most 16 rows go to
 // tree_few.cu.
 //
 // Per block, as in the prefill kernel: S = Q K^T (tcgen05, K-major operands in 128-byte-swizzled shared
@@ -23,7 +23,11 @@
 // What bounds it (B200): up to about 64 rows the pages' read: 64 sequences of 128 .. 8192 tokens, 64 rows,
 // bf16, 1.25 GB in 221 us (5.66 TB/s; the floor is 191), at the GPU's power limit (1000 W, SM clock 1.6
 // GHz). With more rows the softmax between two products: 8 sequences of 32K .. 128K tokens, 256 rows, e4m3,
-// 584 GFLOP in 622 us (940 TFLOP/s, at the power limit; 528 us in a single call).
+// 584 GFLOP in 611 us (955 TFLOP/s, at the power limit; 528 us in a single call). With one tile and e4m3
+// pages shared memory: a block's pages land, are read, written wider and read by the products, with Q 128 KB
+// or 1024 cycles of an SM's 1450 (32 sequences of 4096 tokens, 32/8 heads: 32 rows 97 us, 64 rows 107).
+// Code that runs once a part (masked blocks, the epilogue, Q) mostly waits for its instructions: it is
+// written in rolled loops (e4m3, 64 ragged sequences of 64 rows: 252 us unrolled, 230).
 #include <algorithm>
 #include <type_traits>
 
@@ -74,7 +78,8 @@ struct Layout {
                                              // PV issuer, and with e4m3 four that widen
   static constexpr int kThreads = 32 * (kSoftWarps + (kFp8 ? 8 : 4));
   // Scores of a row that its thread holds at a time: all 64 of a block, or, where registers do not
-  // suffice (768 threads an SM, or the cap's arithmetic), 32 that are read twice from tensor memory.
+  // suffice (768 threads an SM, or the cap's arithmetic), 32 that are read twice from tensor memory (blocks
+  // under masks: 16).
   static constexpr int kHeld = (kFp8 && NT == 1) || kCap ? 32 : 64;
   // P is 2^(s - m + kShift): f16 keeps 7 more binades of small weights before it rounds them away
   // (2^(8 + 7) is still finite); bf16 has float32's range.

@@ -13,9 +13,9 @@
 // most) one by one, under the rows' masks.
 //
 // Measured (B200): 32 sequences of 2048 tokens, 32/32 heads, 5 to 7 nodes, f16, capped: 1.08 GB in 178 us
-// (6.05 TB/s; 245 with the 128-row tiles). 32 sequences of 4096 tokens, 32/8 heads: 16 rows 96.8 us here and
-// 105 there with bf16 pages, 67 and 112 with e4m3; 8 rows 96.8 and 102, 57.6 and 111. 512 items of 16 rows
-// over 1024 tokens: 106 and 127.
+// (6.05 TB/s; 245 with the 128-row tiles). 32 sequences of 4096 tokens, 32/8 heads: 16 rows 97.1 us here and
+// 105 there with bf16 pages, 68.5 and 95.6 with e4m3; 8 rows 95.6 and 102, 58.0 and 93.7. 512 items of 16
+// rows over 1024 tokens: 106 and 127.
 #include <algorithm>
 
 #include "decode_math.cuh"
