@@ -331,8 +331,8 @@ int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache,
                    const pa_tensor* tree_mask, int32_t max_query_len, float scale, float softcap,
                    int32_t num_kv_heads, const pa_decode_opts* opts, void* stream);
 
-/* Workspace bytes that a pa_decode_tree call of these sizes asks for, and that do for every call of smaller ones
- * (0 when no context is split; a call's max_context_len counts, or the table's width where that is 0). Calls that
+/* Workspace bytes that a pa_decode_tree call of these sizes asks for, and that do for every call of smaller ones,
+ * of fewer query or KV heads too (0 when no context is split; a call's max_context_len counts, or the table's width where that is 0). Calls that
  * may overlap on the GPU need workspaces of their own. Host only. */
 size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                       int32_t max_query_len, int32_t max_context_len);

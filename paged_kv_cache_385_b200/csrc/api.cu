@@ -5,7 +5,6 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
-#include <climits>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -271,16 +270,14 @@ size_t tree_workspace(int64_t head_dim, const pa::TreePlan& plan, size_t* ml_off
   return acc + ml + round_up(static_cast<size_t>(plan.spans) * pa::kTreeDescInts * sizeof(int32_t), 256);
 }
 
-// The most that any call of at most these sizes needs, which is what a call asks for: fewer nodes may take a
-// form with more spans, so that what the sizes themselves need would not grow with them.
-size_t tree_workspace_of(int64_t head_dim, int64_t num_seqs, int num_kv_heads, int group, int max_query_len,
+// The most that any call of at most these sizes needs, which is what a call asks for: fewer nodes or heads may
+// take a form with more spans, so that what the sizes themselves need would not grow with them.
+size_t tree_workspace_of(int64_t head_dim, int64_t num_seqs, int num_q_heads, int num_kv_heads, int max_query_len,
                          int64_t max_context_len) {
+  pa::TreePlan plans[pa::kTreeForms];
+  const int n = pa::tree_plans_up_to(num_seqs, num_q_heads, num_kv_heads, max_query_len, max_context_len, plans);
   size_t most = 0;
-  for (const int rows : {pa::kTreeFewRows / 2, pa::kTreeFewRows, pa::kTreeRows, INT_MAX}) {
-    const int nodes = std::min(max_query_len, std::max(1, rows / group));
-    most = std::max(most, tree_workspace(head_dim, pa::tree_plan(num_seqs, num_kv_heads, group, nodes, max_context_len),
-                                         nullptr, nullptr));
-  }
+  for (int i = 0; i < n; ++i) most = std::max(most, tree_workspace(head_dim, plans[i], nullptr, nullptr));
   return most;
 }
 
@@ -1045,7 +1042,7 @@ size_t pa_decode_tree_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int
   if (num_seqs <= 0 || num_kv_heads <= 0 || num_q_heads < num_kv_heads || head_dim <= 0 || max_query_len <= 0 ||
       max_context_len <= 0)
     return 0;
-  return tree_workspace_of(head_dim, num_seqs, num_kv_heads, num_q_heads / num_kv_heads, max_query_len, max_context_len);
+  return tree_workspace_of(head_dim, num_seqs, num_q_heads, num_kv_heads, max_query_len, max_context_len);
 }
 
 int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache,
@@ -1170,7 +1167,7 @@ int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache,
   p.spans = plan.spans;
   size_t ml_off = 0, desc_off = 0;
   if (tree_workspace(D, plan, &ml_off, &desc_off)) {
-    const size_t need = tree_workspace_of(D, B, p.num_kv_heads, p.group, max_query_len, max_ctx);
+    const size_t need = tree_workspace_of(D, B, static_cast<int>(Hq), p.num_kv_heads, max_query_len, max_ctx);
     const size_t have = opts.workspace ? opts.workspace_bytes : 0;
     if (have < need)
       return fail(PA_ERR_WORKSPACE, "contexts of up to %lld tokens need a workspace of %zu bytes (got %zu)", (long long)max_ctx,

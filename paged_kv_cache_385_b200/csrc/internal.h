@@ -208,6 +208,7 @@ struct TreeParams {
 };
 constexpr int kTreeMaxNodes = 256;
 constexpr int kTreeMaskWords = kTreeMaxNodes / 64;
+constexpr int kTreeMaxGroup = 16;
 constexpr int kTreeMaxSpans = 2 * 148;  // two CTAs per SM
 constexpr int kTreeDescInts = 8;
 constexpr int kTreeRows = 128;    // rows of a tile: tcgen05 kernel,
@@ -220,6 +221,11 @@ struct TreePlan {
   bool splits;
 };
 TreePlan tree_plan(int64_t num_seqs, int num_kv_heads, int group, int max_query_len, int64_t max_context_len);
+// Of each form that a batch of at most these sizes (heads included) can take, a plan with as many spans as any of
+// them has; returns how many forms. Growing any size takes no form and no span away.
+constexpr int kTreeForms = 3;
+int tree_plans_up_to(int64_t num_seqs, int num_q_heads, int num_kv_heads, int max_query_len, int64_t max_context_len,
+                     TreePlan (&plans)[kTreeForms]);
 bool tree_few_splits(int64_t max_context_len);
 int tree_few_spans(int64_t num_seqs, int num_kv_heads, int rows, int64_t max_context_len);
 cudaError_t launch_decode_tree_few(KvType kv, QType q, int head_dim, const CUtensorMap& k_map, const CUtensorMap& v_map,

@@ -936,11 +936,24 @@ cudaError_t launch_tiles(const CUtensorMap& km, const CUtensorMap& vm, const Tre
 }  // namespace
 
 bool tree_supported(KvType kv, int head_dim, int group) {
-  return group >= 1 && group <= 16 && (head_dim == 128 || (head_dim == 64 && kv != KvType::E4M3));
+  return group >= 1 && group <= kTreeMaxGroup && (head_dim == 128 || (head_dim == 64 && kv != KvType::E4M3));
 }
 
 // Few rows to a (sequence, KV head) take the warp-level kernel.
 static bool few(int64_t max_query_len, int group) { return max_query_len * group <= kTreeFewRows; }
+
+// (Factors are capped where more cannot matter, so that no product overflows.)
+static int64_t capped(int64_t x) { return std::min<int64_t>(x, 1 << 20); }
+
+static TreePlan tile_plan(int tile_rows, int64_t items, int64_t max_context_len) {
+  TreePlan plan;
+  plan.rows = tile_rows;
+  const int64_t blocks = (max_context_len + kKeys - 1) / kKeys, cost = capped(items) * (blocks + Pol<1>::kItemCost);
+  const int64_t most = kTreeMaxSpans / (tile_rows / kRows);
+  plan.spans = static_cast<int>(std::min<int64_t>(most, std::max<int64_t>(1, (cost + Pol<1>::kMinSpan - 1) / Pol<1>::kMinSpan)));
+  plan.splits = blocks > Pol<1>::kWhole;
+  return plan;
+}
 
 TreePlan tree_plan(int64_t num_seqs, int num_kv_heads, int group, int max_query_len, int64_t max_context_len) {
   TreePlan plan;
@@ -951,15 +964,29 @@ TreePlan tree_plan(int64_t num_seqs, int num_kv_heads, int group, int max_query_
     return plan;
   }
   const int64_t rows = static_cast<int64_t>(max_query_len) * group;
-  plan.rows = rows > kRows ? 2 * kRows : kRows;
-  // (Each factor is capped where more cannot matter, so that no product overflows.)
-  const auto cap = [](int64_t x) { return std::min<int64_t>(x, 1 << 20); };
-  const int64_t items = cap(cap(num_seqs) * num_kv_heads) * cap((rows + plan.rows - 1) / plan.rows);
-  const int64_t blocks = (max_context_len + kKeys - 1) / kKeys, cost = cap(items) * (blocks + Pol<1>::kItemCost);
-  const int64_t most = kTreeMaxSpans / (plan.rows / kRows);
-  plan.spans = static_cast<int>(std::min<int64_t>(most, std::max<int64_t>(1, (cost + Pol<1>::kMinSpan - 1) / Pol<1>::kMinSpan)));
-  plan.splits = blocks > Pol<1>::kWhole;
-  return plan;
+  const int tile_rows = rows > kRows ? 2 * kRows : kRows;
+  return tile_plan(tile_rows, capped(num_seqs) * capped(num_kv_heads * capped((rows + tile_rows - 1) / tile_rows)), max_context_len);
+}
+
+int tree_plans_up_to(int64_t num_seqs, int num_q_heads, int num_kv_heads, int max_query_len, int64_t max_context_len,
+                     TreePlan (&plans)[kTreeForms]) {
+  // At most 16 rows: one item to a (sequence, KV head), most spans in the form of up to 8 rows.
+  plans[0].rows = kTreeFewRows;
+  plans[0].spans = tree_few_spans(num_seqs, num_kv_heads, 1, max_context_len);
+  plans[0].splits = tree_few_splits(max_context_len);
+  int n = 1;
+  // A tile form is reached where a KV head can have its least number of rows. A sequence's tiles: from the heads'
+  // side, a KV head's rows over the tile; from the rows', all heads' rows over the fewest that a tile can have on
+  // average (one tile: its least; two: 257 rows take two items, so 257 / 2). Both bounds hold and grow with the sizes.
+  const int64_t rows = static_cast<int64_t>(num_q_heads) * max_query_len;
+  const int64_t head_rows = static_cast<int64_t>(std::min(num_q_heads, kTreeMaxGroup)) * max_query_len;
+  if (head_rows > kTreeFewRows)
+    plans[n++] = tile_plan(kRows, capped(num_seqs) * capped(std::min<int64_t>(num_kv_heads, rows / (kTreeFewRows + 1))), max_context_len);
+  if (head_rows > kRows) {
+    const int64_t by_heads = num_kv_heads * ((head_rows + 2 * kRows - 1) / (2 * kRows));
+    plans[n++] = tile_plan(2 * kRows, capped(num_seqs) * capped(std::min(by_heads, 2 * rows / (2 * kRows + 1))), max_context_len);
+  }
+  return n;
 }
 
 cudaError_t launch_decode_tree(KvType kv, QType q, int head_dim, const CUtensorMap& km, const CUtensorMap& vm,

@@ -454,3 +454,34 @@ def test_planted_mistakes_are_seen():
     c.masks = right
     c.softcap = 30.0
     assert (np.abs(c.oracle()[0] - want) > c.bound(want, weight)).any()
+
+
+# ---- sizing over models of fewer heads --------------------------------------------------------------
+
+
+@cpu_only
+def test_tree_workspace_does_for_smaller_models():
+    """What is named for the largest sizes does for every call of fewer heads of either kind too: a smaller group
+    takes a form with more spans, fewer KV heads one with longer tiles."""
+    size = pa.pa_decode_tree_workspace_bytes
+    assert size(64, 64, 8, 128, 1, 8192) <= size(64, 128, 8, 128, 1, 8192)
+    assert size(64, 32, 8, 128, 8, 8192) <= size(64, 32, 32, 128, 8, 8192)
+    r = random.Random(1)
+    for _ in range(400):
+        hkv, hq = r.choice([1, 2, 7, 8, 32, 100]), 0
+        hq = hkv * r.choice([1, 2, 3, 4, 8, 16])
+        b, n, c = r.choice([1, 2, 9, r.randint(1, 300)]), r.choice([1, 2, r.randint(1, 256)]), r.choice([60, 129, 250, 260, 321, 3000, 131072])
+        most = size(b, hq, hkv, 128, n, c)
+        for _ in range(12):
+            less_kv = r.randint(1, hkv)
+            group = r.randint(1, min(16, hq // less_kv))
+            less = (r.randint(1, b), group * less_kv, less_kv, 128, r.choice([n, r.randint(1, n)]), r.choice([c, r.randint(1, c)]))
+            assert size(*less) <= most, ((b, hq, hkv, 128, n, c), less)
+    # A call takes the workspace of a larger model.
+    for hq, hkv, n in ((4, 2, 5), (16, 1, 1), (3, 3, 17), (16, 1, 9), (4, 4, 64), (8, 1, 64)):
+        ws = aligned_zeros((size(2, 64, 8, 128, 64, 16 * 4096),), torch.uint8)
+        T = 2 * n
+        a = tree_args(out=aligned_zeros((T, hq, 128), BF), q=aligned_zeros((T, hq, 128), BF), mask=None,
+                      k_cache=aligned_zeros((8, hkv, 16, 128), BF), v_cache=aligned_zeros((8, hkv, 16, 128), BF),
+                      bt=aligned_zeros((2, 4096), I32))
+        assert attend(a, n=n, hkv=hkv, workspace=ws.data_ptr(), workspace_bytes=ws.numel()) == pa.PA_ERR_CUDA, pa.pa_last_error()
