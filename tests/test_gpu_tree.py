@@ -307,3 +307,100 @@ def test_out_of_contract_sequences_are_left_alone(kv, group):
     assert int(word) == pa.PA_DEVERR_BAD_BLOCK
     assert right(got, 0, 5) and right(got, 14, 20)
     assert pa.pa_read_device_error(clear=True) == 0
+
+
+# ---- non-finite rows, empty masks and signs in every form ------------------------------------------------
+# Nodes and group reach the warp-level form (up to 16 rows), one tile (up to 128) and two (above).
+
+FORMS = {"warp": (4, 4), "one_tile": (33, 3), "one_tile_words": (100, 1), "two_tiles": (40, 4), "two_tiles_words": (200, 1),
+         "two_items": (72, 16)}
+
+
+def poison(c, pool, node, rows):
+    """Row `rows[h]` of KV head h in the place of sequence 0's node."""
+    at = c.lens_host[0] - c.counts[0] + node
+    for h, row in enumerate(rows):
+        pool[int(c.bt_host[0, at // 16]), h, at % 16] = row.to(pool.dtype).cuda()
+
+
+@pytest.mark.parametrize("before", [0, 5, 2000])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("kv,cap", [("f16", 0.0), ("bf16", 0.0), ("e4m3", 0.0), ("bf16", 20.0), ("e4m3", 20.0)])
+def test_masked_rows_may_hold_anything_in_every_form(kv, cap, form, before):
+    """Several nodes of one tree, in every word of the masks, hold NaN and infinities."""
+    n, group = FORMS[form]
+    c = TreeCase(kv, 128, 2, group, [n, 3], [n + before, 40], seed=21, softcap=cap, extra_rows=2).to_device()
+    want = c.run().clone()
+    bad = [b for b in (3, 33, 70, 130, 190) if b < n]
+    full = [torch.full((128,), x) for x in (float("nan"), float("inf"))]
+    for i, b in enumerate(bad):
+        poison(c, c.k_cache, b, full if i % 2 else full[::-1])
+        poison(c, c.v_cache, b, full[::-1] if i % 2 else full)
+    got = c.run(out=torch.full_like(c.out, 77.0))
+    sees = torch.tensor([any(m >> b & 1 for b in bad) for m in c.masks[:n]] + [False] * 5).cuda()
+    assert sees.any() and not sees[:n].all()
+    assert torch.equal(got[~sees], want[~sees])
+    assert torch.isnan(got[sees]).all()
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("kv", ["f16", "bf16", "e4m3"])
+def test_values_of_seen_nodes_reach_their_column(kv, form):
+    """Single non-finite elements of drafted V rows, in a context that is cut into parts."""
+    n, group = FORMS[form]
+    c = TreeCase(kv, 128, 2, group, [n], [n + 3000], seed=22).to_device()
+    before = c.run().clone()
+    odd = [float("nan")] * 3 if kv == "e4m3" else [float("inf"), float("-inf"), float("nan")]
+    nodes = [b for b in (1, 33, 70, 130, 190) if b < n]
+    for i, b in enumerate(nodes):
+        at = 3000 + b
+        c.v_cache[int(c.bt_host[0, at // 16]), :, at % 16, 7 + 20 * i] = torch.tensor(odd[i % 3]).to(c.v_cache.dtype).cuda()
+    got = c.run(out=torch.full_like(c.out, 77.0))
+    for i, b in enumerate(nodes):
+        sees = torch.tensor([bool(m >> b & 1) for m in c.masks]).cuda()
+        column = got[sees][..., 7 + 20 * i].float()
+        want = torch.full_like(column, odd[i % 3])
+        assert torch.equal(column.nan_to_num(7.0, 8.0, 9.0), want.nan_to_num(7.0, 8.0, 9.0)), b
+        got[sees, :, 7 + 20 * i] = before[sees, :, 7 + 20 * i]
+    assert torch.equal(got, before)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("kv,cap", [("f16", 0.0), ("bf16", 20.0), ("e4m3", 0.0), ("e4m3", 20.0)])
+def test_rows_that_see_nothing_are_zero_in_every_form(kv, cap, form):
+    n, group = FORMS[form]
+    masks = [0 if i % 3 == 0 else (1 << i if i % 3 == 1 else 1 << (i // 2)) for i in range(n)]
+    c = TreeCase(kv, 128, 2, group, [n], [n], masks=masks, softcap=cap, seed=23, extra_rows=1).to_device()
+    got = c.run()
+    check(c, got)
+    assert torch.all(got[:n:3] == 0)
+    c.masks = [0] * n
+    c.mask.zero_()
+    got = c.run(out=torch.full_like(c.out, 77.0))
+    assert torch.all(got[:n] == 0) and torch.all(got[n:] == 77.0)
+
+
+@pytest.mark.parametrize("before", [0, 2000])
+@pytest.mark.parametrize("form", FORMS)
+def test_rows_whose_scores_are_all_minus_infinity_are_zero(form, before):
+    n, group = FORMS[form]
+    c = TreeCase("bf16", 128, 2, group, [n], [n + before], seed=24).to_device()
+    c.q[..., 0] = c.q[..., 0].abs() + 1
+    c.k_cache[..., 0] = float("-inf")
+    assert torch.all(c.run() == 0)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("kv,q,cap", [("e4m3", "bf16", 0.0), ("e4m3", "f16", 0.0), ("e4m3", "bf16", 4.0), ("bf16", "", 0.0)])
+def test_negative_scales_in_every_form(kv, q, cap, form):
+    n, group = FORMS[form]
+    c = TreeCase(kv, 128, 1, group, [n, 2], [n + 150, 40], seed=26, scale=-0.09, q=q, softcap=cap, extra_rows=1).to_device()
+    check(c, c.run())
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("kv,d", [("f16", 128), ("bf16", 64), ("e4m3", 128)])
+def test_caps_in_every_form(kv, d, form):
+    n, group = FORMS[form]
+    c = TreeCase(kv, d, 1, group, [n, 1], [n + 333, 1], seed=27, softcap=3.0, extra_rows=1).to_device()
+    check(c, c.run())
