@@ -483,8 +483,9 @@ __global__ void __launch_bounds__(Layout<KV, D, kCap, NT>::kThreads, NT == 2 ? 1
     const uint32_t inv_g = (65536u + G - 1) / G;
     // A negative scale turns Q's sign (finish_q), so that the largest product gives the largest score.
     const bool negate = p.score_scale < 0.f;
-    // (A scale of 0 becomes one that makes every finite score 0 and leaves a masked score's -inf.)
-    const float sl2 = fmaxf(fabsf(p.score_scale) * 1.4426950408889634f, 1e-37f);
+    // (A scale of 0 makes an infinite product's score NaN, as 0 times it is; masked scores are selected away by
+    // their bits in both passes, so none of them reaches a product with it.)
+    const float sl2 = fabsf(p.score_scale) * 1.4426950408889634f;
     // Capped scores: cap * tanh(s / cap) = cap - 2 cap / (1 + 2^(u s)), in log2 units.
     const float cap2 = kCap ? p.softcap * 1.4426950408889634f : 0.f;
     // (Of a cap so small that u would overflow, u's sign alone matters.)

@@ -391,6 +391,27 @@ def test_rows_whose_scores_are_all_minus_infinity_are_zero(form, before):
 
 
 @pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("kv,cap", [("f16", 0.0), ("bf16", 20.0)])
+def test_a_scale_of_zero_makes_infinite_products_nan(kv, cap, form):
+    """0 times an infinite product is NaN, for the rows that see its key; the others weigh all that they see alike."""
+    n, group = FORMS[form]
+    c = TreeCase(kv, 128, 2, group, [n], [n + 700], seed=25, scale=0.0, softcap=cap).to_device()
+    want = c.run().clone()
+    check(c, want)
+    spike = torch.zeros(128)
+    spike[5] = float("inf")
+    c.q[..., 5] = 1.0
+    poison(c, c.k_cache, 2, [spike, spike])
+    got = c.run(out=torch.full_like(c.out, 77.0))
+    sees = torch.tensor([bool(m >> 2 & 1) for m in c.masks]).cuda()
+    assert torch.isnan(got[sees]).all()
+    assert torch.equal(got[~sees], want[~sees])
+    at = 100  # a token of the context, which every node sees
+    c.k_cache[int(c.bt_host[0, at // 16]), :, at % 16] = spike.to(c.k_cache.dtype).cuda()
+    assert torch.isnan(c.run()).all()
+
+
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("kv,q,cap", [("e4m3", "bf16", 0.0), ("e4m3", "f16", 0.0), ("e4m3", "bf16", 4.0), ("bf16", "", 0.0)])
 def test_negative_scales_in_every_form(kv, q, cap, form):
     n, group = FORMS[form]
