@@ -19,8 +19,8 @@ import torch
 
 try:
     from . import _views
-except ImportError as e:
-    raise ImportError("the _views module is not built; run `python paged_kv_cache_385_b200/build.py`") from e
+except ImportError:  # built for another Python, or not at all: _pack_views does its work
+    _views = None
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # PAGED_KV_CACHE_LIB points the binding at another build of the library (e.g. a tuning variant).
@@ -195,11 +195,25 @@ def _current_stream() -> int:
     return _raw_stream(torch.cuda.current_device())
 
 
+def _pack_views(tensors: tuple, dtypes: dict, device: int):
+    """_views.pack in Python, where the extension is not built."""
+    views, refs = [], []
+    for i, t in enumerate(tensors):
+        if t is None:
+            refs.append(None)
+            continue
+        if t.get_device() != device or t.dtype not in dtypes or t.dim() > 4:
+            return i
+        views.append(as_pa_tensor(t, "tensor", device=False))
+        refs.append(ctypes.addressof(views[-1]))
+    return views, tuple(refs)
+
+
 def _views_of(names: Sequence[str], tensors: tuple, optional: Sequence[str] = ()):
     """(buffer, addresses) of the pa_tensor views of a call's tensors: None for an absent optional one. Every
     tensor must be on the current device, whose stream the call goes to. Keep the buffer until the call is made."""
     device = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
-    got = _views.pack(tensors, _DTYPES, device)
+    got = (_views.pack if _views else _pack_views)(tensors, _DTYPES, device)
     if not isinstance(got, int):
         for name, t in zip(names, tensors):
             if t is None and name not in optional:

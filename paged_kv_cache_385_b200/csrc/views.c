@@ -80,7 +80,8 @@ static PyObject* pack(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
     PyObject* t = PyTuple_GET_ITEM(args[0], i);
     PyObject* ref;
     if (t == Py_None) {
-      ref = Py_NewRef(Py_None);
+      Py_INCREF(Py_None);
+      ref = Py_None;
     } else {
       const int r = read_tensor(t, args[1], device, &views[i]);
       if (r < 0) goto out;

@@ -425,3 +425,13 @@ def test_caps_in_every_form(kv, d, form):
     n, group = FORMS[form]
     c = TreeCase(kv, d, 1, group, [n, 1], [n + 333, 1], seed=27, softcap=3.0, extra_rows=1).to_device()
     check(c, c.run())
+
+
+def test_calls_without_the_views_extension(monkeypatch):
+    c = TreeCase("bf16", 128, 2, 4, [9, 2], [150, 40], seed=28).to_device()
+    want = c.run().clone()
+    monkeypatch.setattr(pa, "_views", None)
+    assert torch.equal(c.run(out=torch.full_like(c.out, 77.0)), want)
+    c.mask = None
+    c.masks = None
+    check(c, c.run(out=torch.full_like(c.out, 77.0)))

@@ -1,10 +1,12 @@
 """CPU checks of the drafted-token calls: refusals before any CUDA call, malformed descriptors, the
 frequency helper against its formulas, and the oracle's own pins. No device compute here."""
 import ctypes
+import importlib.util
 import math
 import os
 import random
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -485,3 +487,56 @@ def test_tree_workspace_does_for_smaller_models():
                       k_cache=aligned_zeros((8, hkv, 16, 128), BF), v_cache=aligned_zeros((8, hkv, 16, 128), BF),
                       bt=aligned_zeros((2, 4096), I32))
         assert attend(a, n=n, hkv=hkv, workspace=ws.data_ptr(), workspace_bytes=ws.numel()) == pa.PA_ERR_CUDA, pa.pa_last_error()
+
+
+# ---- the binding without its extension ---------------------------------------------------------------
+
+
+def test_import_without_the_views_extension():
+    """The package needs the library alone: without _views the calls marshal their tensors in Python."""
+    code = ("import sys\nsys.modules['paged_kv_cache_385_b200._views'] = None\n"
+            "import torch, paged_kv_cache_385_b200 as pa\nassert pa._views is None\n"
+            "x = torch.zeros(1, dtype=torch.int32)\n"
+            "try:\n    pa.pa_commit_tree(x, x, x, x, x, x, x)\n"
+            "except ValueError as e:\n    assert 'k_cache must be a CUDA tensor' in str(e), e\n"
+            "else:\n    raise AssertionError\nprint(pa.pa_version())\n")
+    got = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert got.returncode == 0 and got.stdout.strip() == pa.pa_version(), got.stderr
+
+
+def test_views_in_python_are_the_extensions():
+    ts = (torch.zeros(3, 4, 8)[:, 1:3], None, torch.zeros(0, 2, dtype=BF), torch.tensor(1, dtype=I32),
+          torch.zeros(2, 3, 4, 5, dtype=F16).permute(3, 0, 2, 1), torch.zeros(2, 6, dtype=E4))
+    bad = ((ts[0], torch.zeros(1, dtype=torch.uint8)), (torch.zeros(1, 1, 1, 1, 1),))
+    with_ext, in_python = pa._views.pack(ts, pa._DTYPES, -1), pa._pack_views(ts, pa._DTYPES, -1)
+    for t, a, b in zip(ts, with_ext[1], in_python[1]):
+        assert (a is None and b is None) if t is None else bytes(pa.PaTensor.from_address(a)) == bytes(pa.PaTensor.from_address(b))
+    for b in bad:
+        assert pa._pack_views(b, pa._DTYPES, -1) == pa._views.pack(b, pa._DTYPES, -1)
+    assert pa._pack_views((ts[0],), pa._DTYPES, 0) == 0  # on another device
+
+
+def test_build_goes_on_without_the_views_extension(tmp_path, monkeypatch):
+    """No C compiler or no Python headers: the library is built all the same, and is not built again for it."""
+    spec = importlib.util.spec_from_file_location("_build_under_test", os.path.join(ROOT, "paged_kv_cache_385_b200", "build.py"))
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    monkeypatch.setattr(b, "LIB", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(b, "VIEWS", str(tmp_path / "_views.so"))
+    monkeypatch.setattr(b, "BUILD", str(tmp_path / "objects"))
+    ran = []
+
+    def run(cmd, **kw):
+        if cmd[0] == "gcc":
+            raise FileNotFoundError("gcc")
+        ran.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(b.subprocess, "run", run)
+    with pytest.warns(UserWarning, match="_views"):
+        assert b.build() == str(tmp_path / "lib.so")
+    assert os.path.exists(tmp_path / "lib.so") and len(ran) == len(b.SOURCES) + 1
+    with pytest.warns(UserWarning, match="_views"):
+        b.build()
+    assert len(ran) == len(b.SOURCES) + 1
