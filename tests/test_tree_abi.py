@@ -540,3 +540,23 @@ def test_build_goes_on_without_the_views_extension(tmp_path, monkeypatch):
     with pytest.warns(UserWarning, match="_views"):
         b.build()
     assert len(ran) == len(b.SOURCES) + 1
+
+
+def test_binding_names_the_tensor_that_is_missing(monkeypatch):
+    """Packing and the check for absent tensors, with host tensors standing for device ones (no library call is made)."""
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    calls = ((pa.pa_rope_and_cache, rope_args, dict(zip(rope_args(), pa._ROPE_ARGS)), ("q", "q_out"), ()),
+             (pa.pa_decode_tree, tree_args, dict(zip(tree_args(), pa._TREE_ARGS)), ("mask",), (5, 0.1, 2)),
+             (pa.pa_commit_tree, commit_args, dict(zip(commit_args(), pa._COMMIT_ARGS)), ("new",), ()))
+    for views in (pa._views, None):
+        monkeypatch.setattr(pa, "_views", views)
+        for call, make, names, optional, rest in calls:
+            for key in make():
+                if key in optional:
+                    keep, refs_ = pa._views_of(list(names.values()), tuple(make(**{key: None}).values()),
+                                               [names[k] for k in optional])
+                    assert [r is None for r in refs_] == [k == key for k in make()]
+                    continue
+                with pytest.raises(ValueError, match=f"^{names[key]} is None$"):
+                    call(*make(**{key: None}).values(), *rest)
