@@ -1156,7 +1156,6 @@ int pa_decode_tree(pa_tensor* out, const pa_tensor* q, const pa_tensor* k_cache,
   p.num_blocks = static_cast<int32_t>(NB);
   p.num_kv_heads = num_kv_heads;
   p.group = static_cast<int32_t>(G);
-  p.max_blocks = static_cast<int32_t>(max_blocks);
   p.max_query_len = max_query_len;
   p.max_context_len = static_cast<int32_t>(max_ctx);
   p.score_scale = scale * k_scale;

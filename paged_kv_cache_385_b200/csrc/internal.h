@@ -191,7 +191,6 @@ struct TreeParams {
   int32_t mask_words;
   int32_t num_tokens;  // T
   int32_t num_seqs, num_blocks, num_kv_heads, group;
-  int32_t max_blocks;
   int32_t max_query_len;
   int32_t max_context_len;
   float score_scale;  // scale * k_scale
