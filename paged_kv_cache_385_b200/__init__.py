@@ -346,6 +346,19 @@ def _error_word_ptr(error_word: Optional[torch.Tensor]) -> Optional[int]:
     return error_word.data_ptr()
 
 
+def _check_scratch(name: str, t: Optional[torch.Tensor]) -> None:
+    """What a drafted-token call's kernels write besides its tensors has to be on the current device too."""
+    if t is None:
+        return
+    device = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    if t.is_cuda and t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{device}")
+    if name == "error_word" and t.numel() == 0:
+        raise ValueError("error_word is empty")
+    if name == "workspace" and not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def pa_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: int = PA_ROPE_PLAIN, factor: float = 1.0,
                      trained_len: int = 0, low: float = 1.0, high: float = 32.0) -> torch.Tensor:
     """Host helper: float32 [rot_dim / 2] rotary frequencies, radians per position (see include/pa.h)."""
@@ -362,6 +375,7 @@ def pa_rope_and_cache(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], 
                       k_scale: float = 1.0, v_scale: float = 1.0, error_word: Optional[torch.Tensor] = None,
                       stream=None) -> None:
     """Rotate new tokens' queries and keys and write keys and values into their slots (see include/pa.h)."""
+    _check_scratch("error_word", error_word)
     opts = _ROPE_OPTS.pack(bool(interleaved), magnitude, k_scale, v_scale, _error_word_ptr(error_word) or 0)
     keep, refs = _views_of(_ROPE_ARGS, (q_out, q, key, value, positions, inv_freq, slot_mapping, k_cache, v_cache),
                            ("q_out", "q"))
@@ -375,6 +389,8 @@ def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_
     """Attention of each sequence's drafted nodes over its paged context (see ``pa_decode_tree`` in
     include/pa.h; ``tree_mask`` None is a chain). ``kw`` builds ``opts``."""
     if opts is None:
+        _check_scratch("workspace", kw.get("workspace"))
+        _check_scratch("error_word", kw.get("error_word"))
         opts = decode_opts(**kw)
     elif kw:
         raise TypeError("pass either opts or keyword options, not both")
@@ -395,6 +411,7 @@ def pa_commit_tree(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: t
                    accepted_lens: torch.Tensor, new_context_lens: Optional[torch.Tensor] = None,
                    error_word: Optional[torch.Tensor] = None, stream=None) -> None:
     """Move each sequence's accepted path to the front of its drafted region (see include/pa.h)."""
+    _check_scratch("error_word", error_word)
     keep, refs = _views_of(_COMMIT_ARGS, (k_cache, v_cache, block_tables, query_start, context_lens, accepted,
                                           accepted_lens, new_context_lens), ("new_context_lens",))
     _check(_lib.pa_commit_tree(*refs, _error_word_ptr(error_word), _stream_handle(stream)), "pa_commit_tree")

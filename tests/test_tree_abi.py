@@ -560,3 +560,43 @@ def test_binding_names_the_tensor_that_is_missing(monkeypatch):
                     continue
                 with pytest.raises(ValueError, match=f"^{names[key]} is None$"):
                     call(*make(**{key: None}).values(), *rest)
+
+
+class Elsewhere:
+    """What the binding asks of a device tensor, for one that lies on a second GPU (or is empty, or has gaps)."""
+    is_cuda, dtype = True, torch.int32
+
+    def __init__(self, device=1, n=64, dense=True):
+        self.device, self.n, self.dense = device, n, dense
+
+    get_device = lambda self: self.device  # noqa: E731
+    numel = lambda self: self.n  # noqa: E731
+    element_size = lambda self: 4  # noqa: E731
+    is_contiguous = lambda self: self.dense  # noqa: E731
+    data_ptr = lambda self: 4096 if self.n else 0  # noqa: E731
+
+
+@cpu_only
+def test_words_and_workspaces_of_another_device_are_refused(monkeypatch):
+    """A kernel that wrote them would fault; an empty error word would silently be the library's own."""
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # (host tensors stand for device ones)
+    monkeypatch.setattr(pa, "_stream_handle", lambda stream: 0)
+    rope_, tree_, commit_ = (lambda **kw: pa.pa_rope_and_cache(*rope_args().values(), **kw),
+                             lambda **kw: pa.pa_decode_tree(*tree_args().values(), 5, 0.1, 2, **kw),
+                             lambda **kw: pa.pa_commit_tree(*commit_args().values(), **kw))
+    for call in (rope_, tree_, commit_):
+        with pytest.raises(ValueError, match="error_word is on cuda:1, the current device is"):
+            call(error_word=Elsewhere())
+        with pytest.raises(ValueError, match="error_word is empty"):
+            call(error_word=Elsewhere(-1, 0))
+        with pytest.raises(pa.PagedAttentionError) as e:  # what is right gets as far as the device
+            call(error_word=Elsewhere(-1))
+        assert e.value.status == pa.PA_ERR_CUDA
+    with pytest.raises(ValueError, match="workspace is on cuda:1, the current device is"):
+        tree_(workspace=Elsewhere())
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        tree_(workspace=Elsewhere(-1, dense=False))
+    with pytest.raises(pa.PagedAttentionError) as e:
+        tree_(workspace=Elsewhere(-1), error_word=Elsewhere(-1))
+    assert e.value.status == pa.PA_ERR_CUDA
