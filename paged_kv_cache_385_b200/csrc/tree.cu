@@ -43,7 +43,7 @@ constexpr int kRows = kTreeRows;  // query rows of a tile
 constexpr int kKeys = 64;         // keys of a block
 // The schedule of items of NT tiles; its units are blocks.
 template <int NT>
-using Pol = tree::Policy<kKeys, NT * kRows, 10, 4, 4>;
+using Pol = tree::Policy<kKeys, NT * kRows, 10, 4, 4, false>;
 using tree::Part;
 constexpr int kParts = 4;  // parts handed on and not yet left by every role
 constexpr uint32_t kQHalf = kRows * 128;  // a 64-element (128-byte) column half of the Q tile

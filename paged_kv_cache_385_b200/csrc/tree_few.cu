@@ -24,7 +24,7 @@
 namespace pa {
 namespace {
 
-using Pol = tree::Policy<16, kTreeFewRows, 4, 8, 6>;  // units are pages
+using Pol = tree::Policy<16, kTreeFewRows, 4, 8, 6, true>;  // units are pages
 using tree::Part;
 
 template <KvType KV, QType QT, int D, int NT, int OCC>

@@ -435,3 +435,50 @@ def test_calls_without_the_views_extension(monkeypatch):
     c.mask = None
     c.masks = None
     check(c, c.run(out=torch.full_like(c.out, 77.0)))
+
+
+def replay_us(call):
+    """Microseconds of a call, from the fastest of some replays of a graph of 20."""
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(20):
+            call()
+    best = float("inf")
+    for _ in range(10):
+        begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        begin.record()
+        graph.replay()
+        end.record()
+        torch.cuda.synchronize()
+        best = min(best, begin.elapsed_time(end) * 50)
+    return best
+
+
+@pytest.mark.parametrize("n", [4, 16, 64])
+def test_slots_without_nodes(n):
+    """A padded batch: hundreds of empty slots before, between and behind the sequences change no row, and cost no
+    multiple of the batch's time (one load's latency each was eight times it)."""
+    real, lens = [n, 1, n], [700, 300, 33 + n]
+    c = TreeCase("bf16", 128, 2, 4, real, lens, masks=None, seed=29).to_device()
+    ws = c.workspace()
+    plain = replay_us(lambda: c.run(workspace=ws))
+    table = c.bt
+    for gap in (1, 7, 8, 9, 600):
+        for before, between, behind in ((gap, 0, 0), (0, gap, 0), (0, 0, gap), (gap, gap, gap)):
+            slots = [before, before + 1 + between, before + 2 + 2 * between]
+            B = slots[-1] + 1 + behind
+            c.bt = torch.full((B, table.shape[1]), -1, dtype=torch.int32, device="cuda")
+            counts, ctx = [0] * B, [0] * B
+            for i, s in enumerate(slots):
+                c.bt[s] = table[i]
+                counts[s], ctx[s] = real[i], lens[i]
+            c.start = torch.tensor(np.concatenate(([0], np.cumsum(counts))), dtype=torch.int32, device="cuda")
+            c.lens = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+            m = pa.pa_decode_tree_workspace_bytes(B, c.hq, c.hkv, 128, n, max(lens))
+            ws = torch.empty(m, dtype=torch.uint8, device="cuda")
+            check(c, c.run(out=torch.full_like(c.out, 77.0), workspace=ws))
+            if gap == 600:
+                took = replay_us(lambda: c.run(workspace=ws))
+                assert took < 2 * plain + 5, (before, between, behind, plain, took)
