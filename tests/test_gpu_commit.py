@@ -180,3 +180,32 @@ def test_a_step_of_drafted_tokens(kv):
     for o, pools in zip(outs, ((kc, vc), plain)):
         pa.pa_decode(o, nxt, *pools, bt, new, scale, hkv, k_scale=ks, v_scale=vs, max_context_len=256)
     assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("kv,group", [("bf16", 4), ("e4m3", 4), ("bf16", 1)])
+def test_the_far_end_of_a_large_pool(kv, group):
+    """A pool of more than 2^32 elements, its last blocks in use: every call gives what it gives in a small one."""
+    c = TreeCase(kv, 128, 8, group, [9, 40], [150, 400], seed=9).to_device()
+    want = c.run().clone()
+    raw = torch.uint8 if kv == "e4m3" else torch.int16
+    blocks = (1 << 32) // (8 * 16 * 128) + 1000
+    off = blocks - c.num_blocks
+    small, far = [c.k_cache, c.v_cache], []
+    for p in small:
+        far.append(torch.zeros(blocks, 8, 16, 128, dtype=p.dtype, device="cuda"))
+        far[-1].view(raw)[off:] = p.view(raw)
+    far_bt = torch.where(c.bt >= 0, c.bt + off, c.bt)
+    g = torch.Generator().manual_seed(10)
+    key, value = (torch.randn(7, 8, 128, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    slots, positions = torch.arange(7, device="cuda") * 13 + 5, torch.arange(7, device="cuda") * 1000
+    inv = pa.pa_rope_inv_freq(128).cuda()
+    accepted = torch.tensor([[0, 3, 7], [1, 20, 39]], dtype=torch.int32, device="cuda")
+    taken = torch.full((2,), 3, dtype=torch.int32, device="cuda")
+    out, bt = torch.full_like(c.out, 77.0), c.bt
+    c.k_cache, c.v_cache, c.bt = *far, far_bt
+    assert torch.equal(c.run(out=out), want)
+    for pools, table, first in ((small, bt, 0), (far, far_bt, 16 * off)):
+        pa.pa_commit_tree(*pools, table, c.start, c.lens, accepted, taken)
+        pa.pa_rope_and_cache(None, None, key, value, positions, inv, slots + first, *pools, k_scale=0.02, v_scale=0.02)
+    for a, b in zip(far, small):
+        assert torch.equal(a.view(raw)[off:], b.view(raw)) and not a.view(raw)[:off].any()

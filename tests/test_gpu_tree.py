@@ -482,3 +482,15 @@ def test_slots_without_nodes(n):
             if gap == 600:
                 took = replay_us(lambda: c.run(workspace=ws))
                 assert took < 2 * plain + 5, (before, between, behind, plain, took)
+
+
+@pytest.mark.parametrize("counts", [[9, 3], [2, 4]])
+def test_rows_before_the_first_sequence(counts):
+    """query_start may begin behind some rows: they are neither read nor written."""
+    c = TreeCase("bf16", 128, 2, 4, counts, [150, 40], seed=30).to_device()
+    want = c.run().clone()
+    q = torch.cat([torch.full_like(c.q[:5], float("nan")), c.q])
+    c.mask = torch.cat([torch.full_like(c.mask[:1].expand(5, -1), -1), c.mask])
+    c.start += 5
+    got = c.run(out=torch.full_like(q, 77.0), q=q)
+    assert torch.equal(got[5:], want) and torch.all(got[:5] == 77.0)
