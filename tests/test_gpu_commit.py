@@ -209,3 +209,49 @@ def test_the_far_end_of_a_large_pool(kv, group):
         pa.pa_rope_and_cache(None, None, key, value, positions, inv, slots + first, *pools, k_scale=0.02, v_scale=0.02)
     for a, b in zip(far, small):
         assert torch.equal(a.view(raw)[off:], b.view(raw)) and not a.view(raw)[:off].any()
+
+
+@pytest.mark.parametrize("group,nodes", [(4, [13, 6, 9]), (1, [3, 5, 2])])
+def test_a_captured_step(group, nodes):
+    """Write, attend and commit captured into one graph: every replay gives what the calls one by one give."""
+    hkv, history = 2, [370, 5, 160]
+    c = TreeCase("bf16", 128, hkv, group, nodes, [h + n for h, n in zip(history, nodes)], seed=11).to_device()
+    T, slots = sum(nodes), []
+    for s, (h, n) in enumerate(zip(history, nodes)):
+        slots += pa.pa_slots_for_positions(c.bt_host, [s] * n, list(range(h, h + n))).tolist()
+    slots = torch.tensor(slots, device="cuda")
+    positions = torch.arange(T, device="cuda") % 7 + 100
+    inv = pa.pa_rope_inv_freq(128).cuda()
+    accepted = torch.tensor([[0, 2], [0, 3], [1, -1]], dtype=torch.int32, device="cuda")
+    taken = torch.tensor([2, 2, 1], dtype=torch.int32, device="cuda")
+    key, value, q = (torch.empty(T, h, 128, dtype=torch.bfloat16, device="cuda") for h in (hkv, hkv, hkv * group))
+    q_out, new, ws = torch.empty_like(q), torch.empty_like(c.lens), c.workspace()
+
+    def step():
+        pa.pa_rope_and_cache(q_out, q, key, value, positions, inv, slots, c.k_cache, c.v_cache)
+        c.run(q=q_out, workspace=ws)
+        pa.pa_commit_tree(c.k_cache, c.v_cache, c.bt, c.start, c.lens, accepted, taken, new)
+
+    def state():
+        return [t.view(torch.int16).clone() for t in (q_out, c.out, c.k_cache, c.v_cache)] + [new.clone()]
+
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    for t in (key, value, q):
+        t.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for seed in (1, 2, 3):
+        g = torch.Generator().manual_seed(seed)
+        fresh = [torch.randn(t.shape, generator=g).to(torch.bfloat16).cuda() for t in (key, value, q)]
+        pools = c.k_cache.clone(), c.v_cache.clone()
+        got = []
+        for run in (graph.replay, step):
+            for t, x in zip((key, value, q, c.k_cache, c.v_cache), (*fresh, *pools)):
+                t.copy_(x)
+            c.out.fill_(77.0), q_out.fill_(77.0), new.fill_(-1)
+            run()
+            torch.cuda.synchronize()
+            got.append(state())
+        assert all(torch.equal(a, b) for a, b in zip(*got))
