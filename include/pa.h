@@ -264,14 +264,15 @@ void pa_rope_opts_init(pa_rope_opts* opts);
  *   q_out, q      [T, Hq, D] device F16/BF16 (one dtype, that of key), last stride 1, 16-B aligned rows;
  *                 q_out may be q itself (same strides), and both may be NULL (keys and values only).
  *   key, value    [T, Hkv, D] as in pa_reshape_and_cache.
- *   positions     [T] device I64, any values: a token's position (a drafted node's is its depth in the
+ *   positions     [T] device I64: a token's position (a drafted node's is its depth in the
  *                 tree past the context, so siblings share one).
  *   inv_freq      [R / 2] device F32: radians per position of each pair (pa_rope_inv_freq, or the
  *                 model's own). The first R elements of a head turn, the others pass unchanged; R is a
  *                 multiple of 8, 8 <= R <= D.
  *   slot_mapping, k_cache, v_cache  as in pa_reshape_and_cache; slot -1 (or one outside the pool, which
  *                 sets PA_DEVERR_BAD_SLOT) writes no key and value, its query row is rotated all the same.
- * With a = positions[t] * inv_freq[i] (formed and reduced in float64), a pair (x, y) becomes
+ * With a = positions[t] * inv_freq[i] (formed and reduced in float64: right to 2^-22 while |a| < 2^28, its error
+ * growing in proportion to |a| beyond), a pair (x, y) becomes
  * magnitude * (x cos a - y sin a, y cos a + x sin a) in float32, rounded once: to nearest even for q_out
  * and 16-bit caches; for E4M3 the unrounded value takes pa_reshape_and_cache's quantisation (no 16-bit
  * rounding in between). Values are stored exactly as pa_reshape_and_cache stores them.

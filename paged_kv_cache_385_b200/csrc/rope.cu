@@ -6,7 +6,8 @@
 // over pairs (i, i + R/2) or (2i, 2i + 1) of the head's first R elements; the rest passes unchanged.
 // Positions reach millions of radians, where a float32 product has lost the angle: turns =
 // position * inv_freq / 2 pi is formed in float64 and its whole part dropped there, and what is left
-// (|turns| <= 1/2) goes to sincospif in float32, an angle error below 2^-22 at any position.
+// (|turns| <= 1/2) goes to sincospif in float32. Three roundings of 2^-53 of the turns and one of 2^-26 of a
+// turn: an angle error below 2^-22 while |position * inv_freq| < 2^28, and growing with it beyond.
 //
 // Every element is read and written once, so HBM bandwidth (or, for a decode step's few tokens,
 // latency) bounds it. One CTA per token: its R/2 sines are made once, in shared memory, for all

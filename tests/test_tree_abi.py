@@ -7,6 +7,7 @@ import os
 import random
 import subprocess
 import sys
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -600,3 +601,23 @@ def test_words_and_workspaces_of_another_device_are_refused(monkeypatch):
     with pytest.raises(pa.PagedAttentionError) as e:
         tree_(workspace=Elsewhere(-1), error_word=Elsewhere(-1))
     assert e.value.status == pa.PA_ERR_CUDA
+
+
+def test_angles_hold_their_bound():
+    """The kernel's float64 turns, rounded to float32, against exact ones: 2^-22 of an angle up to 2^28 radians (3 * 2^-53
+    of at most 2^25.4 turns and 2^-26 of a turn, times 2 pi: 2^-23.4 + 2^-23.3), and no such bound far beyond it."""
+    pi = Fraction(int("314159265358979323846264338327950288419716939937510582097494459"), 10 ** 62)
+
+    def worst(top, seed):
+        r, most = random.Random(seed), 0.0
+        for _ in range(3000):
+            f = float(np.float32(r.uniform(0.01, 1.0)))
+            pos = int(r.uniform(0.5, 1.0) * top / f)
+            turns = np.float64(pos) * np.float64(f) * np.float64(0.15915494309189535)
+            left = Fraction(float(np.float32(turns - np.rint(turns))))
+            off = (Fraction(pos) * Fraction(f) / (2 * pi) - left) % 1
+            most = max(most, 2 * math.pi * float(min(off, 1 - off)))
+        return most
+
+    assert worst(2.0 ** 28, 1) < 2.0 ** -22 and worst(1e6, 2) < 2.0 ** -23
+    assert worst(2.0 ** 34, 3) > 2.0 ** -22
