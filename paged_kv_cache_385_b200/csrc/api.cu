@@ -1,7 +1,7 @@
 // C-ABI entry points of libpagedattn: argument validation, TMA descriptor encoding, dispatch.
 // Host code only. Every argument error is found here before the first device call; the kernels
-// live in decode.cu, decode_units.cu, multiquery.cu, prefill_tc.cu, tree.cu, tree_commit.cu, rope.cu, cache.cu,
-// no_alloc.cu and selftest.cu.
+// live in decode.cu, decode_units.cu, multiquery.cu, prefill_tc.cu, tree.cu, tree_few.cu, tree_commit.cu, rope.cu,
+// cache.cu, no_alloc.cu and selftest.cu.
 #include <cudaTypedefs.h>
 
 #include <atomic>

@@ -10,8 +10,8 @@
 // products. NT = 2 where a KV head has more than 128 rows: one CTA to an SM, whose two tiles share each
 // block's pages (half the copies, and with e4m3 half the widening) and overlap one another. Measured, 16
 // sequences of 8192 tokens, 32/8 heads: 132 rows 197 us (NT = 1) and 155 (NT = 2), 256 rows 231 and 184,
-// 400 rows 427 and 327; with e4m3 pages 179 and 149, 205 and 172, 383 and 305. At most 16 rows go to
-// tree_few.cu.
+// 400 rows 427 and 327; with e4m3 pages 179 and 149, 205 and 172, 383 and 305 (back to back, at the power limit;
+// in a short burst the 256 rows take 157 and 160). At most 16 rows go to tree_few.cu.
 //
 // Per block, as in the prefill kernel: S = Q K^T (tcgen05, K-major operands in 128-byte-swizzled shared
 // memory, two S buffers in tensor memory), softmax by 4 warps to a tile with a row per thread, P over S in
@@ -20,12 +20,21 @@
 // issuer (owner of the tensor memory), a TMA producer of V, a PV issuer. e4m3 pages land as they are (the
 // first producer brings both) and two pairs of warps widen them into the f16 operand tiles.
 //
+// Roundings. Scores, references, sums and O are float32. P is rounded to the operands' 16-bit type: both operands
+// of a product have one type, V's is the pages' (e4m3 is exact in f16), and wider ones would halve the products'
+// rate. Rows are off by that and by their own rounding: with bf16 pages 0.0023 of their norm from the exact ones,
+// where P in float32 would leave 0.0017. bf16 queries of e4m3 pages become f16: exact from 2^-14 to
+// 65504, to 2^-25 below.
+//
 // What bounds it (B200): up to about 64 rows the pages' read: 64 sequences of 128 .. 8192 tokens, 64 rows,
 // bf16, 1.25 GB in 221 us (5.66 TB/s; the floor is 191), at the GPU's power limit (1000 W, SM clock 1.6
 // GHz). With more rows the softmax between two products: 8 sequences of 32K .. 128K tokens, 256 rows, e4m3,
 // 584 GFLOP in 611 us (955 TFLOP/s, at the power limit; 528 us in a single call). With one tile and e4m3
 // pages shared memory: a block's pages land, are read, written wider and read by the products, with Q 128 KB
-// or 1024 cycles of an SM's 1450 (32 sequences of 4096 tokens, 32/8 heads: 32 rows 97 us, 64 rows 107).
+// or 1024 cycles of an SM's 1450 (32 sequences of 4096 tokens, 32/8 heads: 32 rows 97 us, 64 rows 107). With two
+// tiles a block costs an SM 1880 cycles (16-bit pages; e4m3 2020: the slope over 8K to 32K tokens, at the sampled
+// clocks). 16 sequences of 8192 tokens, 256 rows, bf16, in a short burst, 155 us: first scores 8, the median CTA's
+// 111 blocks with its changes of part 115, its last rows 5, the slowest CTA 12 behind it, the join 15.
 // Code that runs once a part (masked blocks, the epilogue, Q) mostly waits for its instructions: it is
 // written in rolled loops (e4m3, 64 ragged sequences of 64 rows: 252 us unrolled, 230).
 #include <algorithm>

@@ -16,6 +16,11 @@
 // (6.05 TB/s; 245 with the 128-row tiles). 32 sequences of 4096 tokens, 32/8 heads: 16 rows 97.1 us here and
 // 105 there with bf16 pages, 68.5 and 95.6 with e4m3; 8 rows 95.6 and 102, 58.0 and 93.7. 512 items of 16
 // rows over 1024 tokens: 106 and 127.
+//
+// 16-bit pages are bounded by their read. e4m3 pages, of half the bytes, are not (41 us of read in those 68.5 and
+// 58.0): a page's widening, products and softmax form one dependent chain, and registers (255 and 164) leave a
+// scheduler two or three warps to hide it with. 33 and 38% of issue slots are used, no pipe above 35%; the
+// largest stall is the wait for the instruction before.
 #include <algorithm>
 
 #include "decode_math.cuh"

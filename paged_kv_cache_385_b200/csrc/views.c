@@ -1,8 +1,8 @@
 /* _views.pack: the pa_tensor views of a call's torch tensors, filled in one pass through the CPython API.
  *
  * The binding's calls take six to nine tensors. Reading a tensor's pointer, dtype, shape and strides
- * and packing them took 0.9 us a tensor in Python, more than a small call's kernel takes on the GPU;
- * here it takes 0.3. No torch header is used: the tensors are read through their public methods. */
+ * and packing them takes 0.9 to 1.3 us a tensor in Python, for a call more than a small kernel takes on the GPU;
+ * here it takes 0.3 (a 64-token rope call 10.5 us of host time for 16.9, a commit 9.1 for 15.5). No torch header is used: the tensors are read through their public methods. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <string.h>
